@@ -395,6 +395,117 @@ int km_finalize_sums(const double* sums, const double* counts, int K, int D, int
 int km_plan_describe(int op, int B, int64_t N, int D, int K, int dtype, int64_t chunk_rows, int64_t* out);
 
 /*
+ * Soft assignment.  The differentiable side of an assignment, for callers that
+ * train a codebook or a router next to (or with) the clusters: points kept in
+ * 8 bits, their scores against the centroids, the gradients of those scores
+ * taken from the 8-bit points, and a loss on how evenly the picks spread.  The
+ * paper has no counterpart (§5 Significance names sparse routing and vector
+ * quantisation as uses).
+ *
+ *   km_quantize -> km_scores -> (a pick per point, e.g. km_assign's) ->
+ *   km_balance -> km_balance_grad -> km_scores_grad
+ *
+ * These calls share the conventions at the top of this file, except:
+ *  - shapes: 1 <= B <= 65536, 0 <= N < 2^31 (no points: sums are 0),
+ *    1 <= D <= 65536, 1 <= K <= 2^20, any D and K (no multiple of 8, and K
+ *    may exceed N);
+ *  - infinities and NaN have the meaning each call gives.
+ *
+ * Points in 8 bits.  A set of points [B][N][D] is
+ *   q      [B][N][ld] bytes, ld = D rounded up to a multiple of 16: e4m3
+ *          values (16-byte aligned; the ld - D bytes behind a row are written
+ *          as zero and never read);
+ *   scale  [B][N][nb] bytes, nb = ceil(D / 128): e8m0 exponents, byte s
+ *          standing for 2^(s - 127) and 255 for NaN;
+ * and coordinate d of a point stands for q[d] * scale[d / 128].
+ */
+typedef enum km_soft_op {
+  KM_SOFT_SCORES = 0,      /* km_scores */
+  KM_SOFT_SCORES_GRAD = 1, /* km_scores_grad (dtype of dS) */
+  KM_SOFT_BALANCE = 2      /* km_balance (D ignored) */
+} km_soft_op;
+
+/*
+ * Bytes of workspace the operator needs (0 if the shape is invalid or
+ * unsupported; km_last_error() says why).  Never O(N*K), except that
+ * KM_SOFT_SCORES_GRAD holds a copy of dS of an odd layout: float32, or K not a
+ * multiple of 8.
+ */
+size_t km_soft_workspace_size(int op, int B, int64_t N, int D, int K, int dtype);
+
+/*
+ * Points to 8 bits.  A block's scale is the smallest power of two 2^e, e >=
+ * -117, with max|x| <= 448 * 2^e, and q = x / 2^e rounded to nearest even: an
+ * error of at most 2^-4 of |x|, or of 2^-10 * 2^e for the values below
+ * 2^-6 * 2^e.  A block that holds an infinity or a NaN stands for NaN.
+ *   X  [B][N][D] dtype, device, read only.
+ */
+int km_quantize(const void* X, int B, int64_t N, int D, int dtype, uint8_t* q, uint8_t* scale, void* stream);
+
+/* The values the 8-bit points stand for, X [B][N][D] dtype (exact in either type for the scales of km_quantize). */
+int km_dequantize(const uint8_t* q, const uint8_t* scale, int B, int64_t N, int D, int dtype, void* X, void* stream);
+
+/*
+ * Scores of every point against every centroid, both in 8 bits:
+ *   S[b][i][k] = bias[b][k] + alpha * sum_d x[b][i][d] * c[b][k][d]
+ * on the tensor cores with float32 sums.  alpha = 2 / t and bias = -|c|^2 / t
+ * give the logits of softmax(-|x - c|^2 / t).
+ *   bias  [B][K] float, device; may be NULL.
+ *   S     [B][N][K] dtype, device, written (rounded once).
+ */
+int km_scores(const uint8_t* xq, const uint8_t* xs, const uint8_t* cq, const uint8_t* cs, const float* bias,
+              float alpha, int B, int64_t N, int D, int K, int dtype, void* S, void* workspace,
+              size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of km_scores with respect to the values that the 8-bit points and
+ * centroids stand for, given dS [B][N][K] (dtype):
+ *   dX    [B][N][D] dx_dtype = alpha * dS c       (may be NULL)
+ *   dC    [B][K][D] float    = alpha * dS^T x     (may be NULL)
+ *   dbias [B][K] float       = column sums of dS  (may be NULL)
+ * A float32 dS enters the tensor cores as three bf16 pieces (24 bits); sums
+ * are float32, in a fixed order (bitwise reproducible).  dS must be 16-byte
+ * aligned.
+ */
+int km_scores_grad(const void* dS, const uint8_t* xq, const uint8_t* xs, const uint8_t* cq, const uint8_t* cs,
+                   float alpha, int B, int64_t N, int D, int K, int dtype, int dx_dtype, void* dX, float* dC,
+                   float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Balance loss of a soft assignment and the members per cluster.  With p_i the
+ * softmax of row i of S, M the number of valid points, T picks per point and
+ * f_k = counts_k / (M * T):
+ *   loss = K * sum_k f_k * (mean over valid i of p_ik)
+ * 1 when the picks or the probabilities are uniform, up to K when all of both
+ * fall on one cluster.
+ *   S       [B][N][K] dtype, 16-byte aligned.  Entries of -inf have
+ *           probability 0; a row of nothing but -inf has none at all and adds
+ *           nothing to the mean.  A NaN or +inf in a valid row makes the loss NaN.
+ *   idx     [B][N][T] int32: the picks; a value outside [0, K) is no pick.
+ *   valid   [B][N] bytes, 0 = not a point (its S and idx are not looked at);
+ *           NULL = all valid.
+ *   loss    [B] float; 0 when an instance has no valid point.
+ *   counts  [B][K] int32: picks per cluster; rows [B] int32: M.
+ *   lse, dot [B][N] float: each row's logsumexp and sum_k f_k p_ik (0 and 0
+ *           where not valid), which km_balance_grad takes.
+ * N * T < 2^31.  Results are bitwise reproducible.
+ */
+int km_balance(const void* S, const int32_t* idx, const uint8_t* valid, int B, int64_t N, int K, int T, int dtype,
+               float* loss, int32_t* counts, int32_t* rows, float* lse, float* dot, void* workspace,
+               size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of km_balance's loss with respect to S (the counts are constants):
+ *   dS[b][i][k] = grad[b] * (K / M) * p_ik * (f_k - dot_i),
+ * 0 in rows that are not valid.  S, valid, counts, rows, lse and dot are those
+ * of the forward call; grad [B] float is the loss's own gradient (NULL: 1).
+ * dS [B][N][K] dtype, 16-byte aligned, must not overlap S.
+ */
+int km_balance_grad(const void* S, const uint8_t* valid, const int32_t* counts, const int32_t* rows, const float* lse,
+                    const float* dot, const float* grad, int B, int64_t N, int K, int T, int dtype, void* dS,
+                    void* stream);
+
+/*
  * Baselines (not used by the fit).  The two strategies "Flash-KMeans" (§1
  * Problem) says FlashAssign and the Sort-Inverse Update replace, for measuring
  * the method against them on the same device:

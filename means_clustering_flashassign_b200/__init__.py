@@ -19,7 +19,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -29,11 +29,14 @@ __all__ = ["KMError", "library", "library_path", "workspace_size", "assign", "up
            "workspace_status", "selftest_timeout", "argsort", "fit_profile", "launch_count", "assign_static",
            "ablation_assign_materialized", "ablation_update_atomic", "plan", "update_accumulate",
            "finalize_sums", "fit_data_parallel", "pack_layout", "exchange_packed", "fit_source", "FitGraph",
+           "Quantized", "quantize", "dequantize", "scores", "scores_grad", "Balance", "balance", "balance_grad",
+           "soft_workspace_size", "SOFT_SCORES", "SOFT_SCORES_GRAD", "SOFT_BALANCE",
            "OP_ASSIGN", "OP_UPDATE", "OP_FIT", "OP_FIT_HOST",
            "OP_ARGSORT",
            "F32", "BF16", "EXPORTS"]
 
 OP_ASSIGN, OP_UPDATE, OP_FIT, OP_FIT_HOST, OP_ARGSORT = 0, 1, 2, 3, 4
+SOFT_SCORES, SOFT_SCORES_GRAD, SOFT_BALANCE = 0, 1, 2
 F32, BF16 = 0, 1
 STATUS = {0: "KM_OK", 1: "KM_ERR_INVALID_ARG", 2: "KM_ERR_UNSUPPORTED", 3: "KM_ERR_CUDA",
           4: "KM_ERR_WORKSPACE", 5: "KM_ERR_TIMEOUT", 6: "KM_ERR_INJECTED"}
@@ -42,7 +45,8 @@ EXPORTS = ["km_version", "km_status_string", "km_last_error", "km_workspace_size
            "km_launch_count", "km_assign_static", "km_ablation_workspace_size", "km_ablation_assign_materialized",
            "km_ablation_update_atomic", "km_plan_describe", "km_update_accumulate", "km_finalize_sums",
            "km_fit_source", "km_fit_graph_create", "km_fit_graph_launch", "km_fit_graph_elapsed",
-           "km_fit_graph_destroy"]
+           "km_fit_graph_destroy", "km_soft_workspace_size", "km_quantize", "km_dequantize", "km_scores",
+           "km_scores_grad", "km_balance", "km_balance_grad"]
 
 _lock = threading.Lock()
 _lib = None
@@ -103,6 +107,15 @@ def library() -> ctypes.CDLL:
             L.km_fit_graph_launch.argtypes = [P, P]
             L.km_fit_graph_elapsed.argtypes = [P, P]
             L.km_fit_graph_destroy.argtypes = [P]
+            L.km_soft_workspace_size.argtypes = [I, I, I64, I, I, I]
+            L.km_soft_workspace_size.restype = SZ
+            F = ctypes.c_float
+            L.km_quantize.argtypes = [P, I, I64, I, I, P, P, P]
+            L.km_dequantize.argtypes = [P, P, I, I64, I, I, P, P]
+            L.km_scores.argtypes = [P, P, P, P, P, F, I, I64, I, I, I, P, P, SZ, P]
+            L.km_scores_grad.argtypes = [P, P, P, P, P, F, I, I64, I, I, I, I, P, P, P, P, SZ, P]
+            L.km_balance.argtypes = [P, P, P, I, I64, I, I, I, P, P, P, P, P, P, SZ, P]
+            L.km_balance_grad.argtypes = [P, P, P, P, P, P, P, I, I64, I, I, I, P, P]
             for f in EXPORTS:
                 getattr(L, f).restype = getattr(L, f).restype or I
             _lib = L
@@ -711,3 +724,259 @@ def selftest_timeout(limit_ns: int = 1_000_000, device="cuda") -> int:
     """Run the bounded-wait self-test kernel; returns the status it reports."""
     ws = torch.zeros(256, dtype=torch.uint8, device=device)
     return int(library().km_selftest_timeout(_ptr(ws), ws.numel(), int(limit_ns), _stream(None)))
+
+
+# ------------------------------------------------------------ soft assignment
+class Quantized(NamedTuple):
+    """Points in 8 bits: data float8_e4m3fn (..., N, D), rows ceil(D / 16) * 16
+    bytes apart, and scale float8_e8m0fnu (..., N, ceil(D / 128)), one power of
+    two per 128 coordinates; coordinate d stands for data[d] * scale[d // 128]."""
+    data: torch.Tensor
+    scale: torch.Tensor
+
+
+class Balance(NamedTuple):
+    """What balance() returns: the loss float32 [B], the picks per cluster int32
+    (K,) or (B, K), and what its gradient needs: the valid points int32 [B], each
+    row's logsumexp and sum of p * share float32 (N,) or (B, N), and the picks
+    per point."""
+    loss: torch.Tensor
+    counts: torch.Tensor
+    rows: torch.Tensor
+    lse: torch.Tensor
+    dot: torch.Tensor
+    picks: int
+
+
+def soft_workspace_size(op: int, B: int, N: int, D: int, K: int, dtype: int) -> int:
+    n = library().km_soft_workspace_size(op, B, N, D, K, dtype)
+    if n == 0:
+        raise KMError(2, library().km_last_error().decode(errors="replace"))
+    return int(n)
+
+
+class _on:
+    """Device and stream of a call: outputs and workspaces allocated inside
+    belong to the stream the kernels run on."""
+
+    def __init__(self, device, stream):
+        self._d = torch.cuda.device(device)
+        self._s = torch.cuda.stream(stream) if stream is not None else None
+
+    def __enter__(self):
+        self._d.__enter__()
+        if self._s is not None:
+            self._s.__enter__()
+
+    def __exit__(self, *a):
+        if self._s is not None:
+            self._s.__exit__(*a)
+        self._d.__exit__(*a)
+
+
+def _soft_workspace(op, B, N, D, K, dtype, device, workspace):
+    need = soft_workspace_size(op, B, N, D, K, dtype)
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    _check_tensor(workspace, "workspace", device, torch.uint8)
+    if workspace.numel() < need:
+        raise ValueError(f"workspace has {workspace.numel()} bytes, needs {need}")
+    return workspace
+
+
+def _soft_dtype(dtype) -> int:
+    if dtype == torch.bfloat16:
+        return BF16
+    if dtype == torch.float32:
+        return F32
+    raise TypeError(f"the type must be bfloat16 or float32, got {dtype}")
+
+
+def _new_quantized(lead, D, device) -> Quantized:
+    ld = (D + 15) // 16 * 16
+    data = torch.empty(*lead, ld, dtype=torch.float8_e4m3fn, device=device)
+    scale = torch.empty(*lead, (D + 127) // 128, dtype=torch.float8_e8m0fnu, device=device)
+    return Quantized(data[..., :D], scale)
+
+
+def _check_quantized(q, name: str, device=None):
+    """Shape (B, N, D, batched) of 8-bit points, their layout checked: dense
+    rows ceil(D / 16) * 16 bytes apart and dense scales of the same points."""
+    if not isinstance(q, tuple) or len(q) != 2:
+        raise TypeError(f"{name} must be Quantized (data, scale)")
+    data, scale = q
+    if not data.is_cuda or not scale.is_cuda:
+        raise ValueError(f"{name} must be CUDA tensors")
+    if data.dtype != torch.float8_e4m3fn or scale.dtype != torch.float8_e8m0fnu:
+        raise TypeError(f"{name} must be float8_e4m3fn data and float8_e8m0fnu scale, got {data.dtype}, {scale.dtype}")
+    B, N, D, batched = _shape3(data, name)
+    ld = (D + 15) // 16 * 16
+    want = ((N * ld, ld, 1) if batched else (ld, 1))
+    if any(n > 1 and s != w for n, s, w in zip(data.shape, data.stride(), want)):
+        raise ValueError(f"rows of {name}.data must be dense and {ld} bytes apart")
+    if data.numel() and data.data_ptr() % 16:
+        raise ValueError(f"{name}.data must be 16-byte aligned")
+    if data.numel() and data.untyped_storage().nbytes() - data.storage_offset() < B * N * ld:
+        raise ValueError(f"the last row of {name}.data must have {ld} bytes")
+    shp = (*data.shape[:-1], (D + 127) // 128)
+    _check_tensor(scale, f"{name}.scale", data.device, None, shp)
+    if device is not None and data.device != device:
+        raise ValueError(f"{name} is on {data.device}, the points are on {device}")
+    return B, N, D, batched
+
+
+def quantize(X: torch.Tensor, *, out: Optional[Quantized] = None, stream=None) -> Quantized:
+    """Points (N, D) or (B, N, D), bf16 or f32, kept in 8 bits: half or a quarter
+    of the bytes between a forward and a backward pass, and the operand of
+    scores() and scores_grad().  See km_quantize for the rounding."""
+    _contig_cuda(X, "X")
+    B, N, D, _ = _shape3(X, "X")
+    dt = _dtype_code(X)
+    _check_stream(stream, X.device)
+    with _on(X.device, stream):
+        if out is None:
+            out = _new_quantized(X.shape[:-1], D, X.device)
+        elif out.data.shape != X.shape:
+            raise ValueError(f"out must have shape {tuple(X.shape)}, got {tuple(out.data.shape)}")
+        _check_quantized(out, "out", X.device)
+        _check(library().km_quantize(_ptr(X), B, N, D, dt, _ptr(out.data), _ptr(out.scale), _stream(None)))
+    return out
+
+
+def dequantize(q: Quantized, dtype: torch.dtype = torch.bfloat16, *, out=None, stream=None) -> torch.Tensor:
+    """The values 8-bit points stand for, in bf16 or f32 (exact in both)."""
+    B, N, D, _ = _check_quantized(q, "q")
+    dt = _soft_dtype(dtype)
+    dev = q.data.device
+    _check_stream(stream, dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(q.data.shape, dtype=dtype, device=dev)
+        _check_tensor(out, "out", dev, dtype, q.data.shape)
+        _check(library().km_dequantize(_ptr(q.data), _ptr(q.scale), B, N, D, dt, _ptr(out), _stream(None)))
+    return out
+
+
+def _score_args(X, C, stream):
+    B, N, D, batched = _check_quantized(X, "X")
+    dev = X.data.device
+    Bc, K, Dc, batched_c = _check_quantized(C, "C", dev)
+    if Bc != B or Dc != D or batched_c != batched:
+        raise ValueError("C must match X in batch and D")
+    _check_stream(stream, dev)
+    return B, N, D, K, batched, dev
+
+
+def scores(X: Quantized, C: Quantized, *, bias: Optional[torch.Tensor] = None, alpha: float = 1.0,
+           dtype: torch.dtype = torch.float32, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """Scores of 8-bit points against 8-bit centroids: bias + alpha * x . c for
+    every pair, (N, K) or (B, N, K) in `dtype` (bf16 or f32).  bias float32 (K,)
+    or (B, K).  alpha = 2 / t and bias = -|c|^2 / t give the logits of a soft
+    assignment by distance."""
+    B, N, D, K, batched, dev = _score_args(X, C, stream)
+    dt = _soft_dtype(dtype)
+    shp = (B, N, K) if batched else (N, K)
+    if bias is not None:
+        _check_tensor(bias, "bias", dev, torch.float32, (B, K) if batched else (K,))
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(shp, dtype=dtype, device=dev)
+        _check_tensor(out, "out", dev, dtype, shp)
+        ws = _soft_workspace(SOFT_SCORES, B, N, D, K, dt, dev, workspace)
+        _check(library().km_scores(_ptr(X.data), _ptr(X.scale), _ptr(C.data), _ptr(C.scale), _ptr(bias), alpha, B, N, D,
+                                   K, dt, _ptr(out), _ptr(ws), ws.numel(), _stream(None)))
+    return out
+
+
+def scores_grad(dS: torch.Tensor, X: Quantized, C: Quantized, *, alpha: float = 1.0,
+                dtype: Optional[torch.dtype] = None, want_dX: bool = True, want_dC: bool = True,
+                want_dbias: bool = True, workspace=None, stream=None):
+    """Gradients of scores() for the gradient dS (bf16 or f32) of its result,
+    with respect to the values the 8-bit X and C stand for.
+
+    Returns (dX in `dtype`, by default dS's, dC float32, dbias float32), None for
+    those not wanted."""
+    _contig_cuda(dS, "dS")
+    B, N, D, K, batched, dev = _score_args(X, C, stream)
+    _check_tensor(dS, "dS", dev, None, (B, N, K) if batched else (N, K))
+    dt = _dtype_code(dS)
+    dtype = dS.dtype if dtype is None else dtype
+    dxt = _soft_dtype(dtype)
+    if not (want_dX or want_dC or want_dbias):
+        raise ValueError("one of dX, dC and dbias must be wanted")
+    lead = (B,) if batched else ()
+    with _on(dev, stream):
+        dX = torch.empty((*lead, N, D), dtype=dtype, device=dev) if want_dX else None
+        dC = torch.empty((*lead, K, D), dtype=torch.float32, device=dev) if want_dC else None
+        db = torch.empty((*lead, K), dtype=torch.float32, device=dev) if want_dbias else None
+        ws = _soft_workspace(SOFT_SCORES_GRAD, B, N, D, K, dt, dev, workspace)
+        _check(library().km_scores_grad(_ptr(dS), _ptr(X.data), _ptr(X.scale), _ptr(C.data), _ptr(C.scale), alpha, B, N,
+                                        D, K, dt, dxt, _ptr(dX), _ptr(dC), _ptr(db), _ptr(ws), ws.numel(),
+                                        _stream(None)))
+    return dX, dC, db
+
+
+def _valid_mask(valid, shape, device):
+    if valid is None:
+        return None
+    if valid.dtype not in (torch.bool, torch.uint8):
+        raise ValueError(f"valid must be bool or uint8, got {valid.dtype}")
+    return _check_tensor(valid, "valid", device, None, shape)
+
+
+def balance(S: torch.Tensor, idx: torch.Tensor, *, valid: Optional[torch.Tensor] = None, workspace=None,
+            stream=None) -> Balance:
+    """Balance loss of the soft assignment softmax(S) under the picks idx, and
+    the picks per cluster.  S (N, K) or (B, N, K) bf16/f32; idx int32 (N,) or
+    (B, N), or with T picks per point (N, T) or (B, N, T); valid (N,) or (B, N)
+    bool: the points that count.  See km_balance."""
+    _contig_cuda(S, "S")
+    B, N, K, batched = _shape3(S, "S")
+    dt = _dtype_code(S)
+    lead = (B, N) if batched else (N,)
+    T = idx.shape[-1] if idx.dim() == len(lead) + 1 else 1
+    if T < 1:
+        raise ValueError("idx must hold at least one pick per point")
+    _check_tensor(idx, "idx", S.device, torch.int32, (*lead, T) if idx.dim() == len(lead) + 1 else lead)
+    valid = _valid_mask(valid, lead, S.device)
+    _check_stream(stream, S.device)
+    dev = S.device
+    with _on(dev, stream):
+        loss = torch.empty(B, dtype=torch.float32, device=dev)
+        counts = torch.empty((B, K) if batched else (K,), dtype=torch.int32, device=dev)
+        rows = torch.empty(B, dtype=torch.int32, device=dev)
+        lse = torch.empty(lead, dtype=torch.float32, device=dev)
+        dot = torch.empty(lead, dtype=torch.float32, device=dev)
+        ws = _soft_workspace(SOFT_BALANCE, B, N, 1, K, dt, dev, workspace)
+        _check(library().km_balance(_ptr(S), _ptr(idx), _ptr(valid), B, N, K, T, dt, _ptr(loss), _ptr(counts),
+                                    _ptr(rows), _ptr(lse), _ptr(dot), _ptr(ws), ws.numel(), _stream(None)))
+    return Balance(loss, counts, rows, lse, dot, T)
+
+
+def balance_grad(S: torch.Tensor, bal: Balance, *, grad: Optional[torch.Tensor] = None,
+                 valid: Optional[torch.Tensor] = None, out=None, stream=None) -> torch.Tensor:
+    """Gradient of balance()'s loss with respect to S (S's type), given what
+    balance() returned for the same S and valid; grad float32 [B] is the
+    gradient of the loss itself (1 if not given)."""
+    _contig_cuda(S, "S")
+    B, N, K, batched = _shape3(S, "S")
+    dt = _dtype_code(S)
+    dev = S.device
+    lead = (B, N) if batched else (N,)
+    _check_tensor(bal.counts, "counts", dev, torch.int32, (B, K) if batched else (K,))
+    _check_tensor(bal.rows, "rows", dev, torch.int32, (B,))
+    _check_tensor(bal.lse, "lse", dev, torch.float32, lead)
+    _check_tensor(bal.dot, "dot", dev, torch.float32, lead)
+    valid = _valid_mask(valid, lead, dev)
+    if grad is not None:
+        _check_tensor(grad, "grad", dev, torch.float32, (B,))
+    _check_stream(stream, dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty_like(S)
+        _check_tensor(out, "out", dev, S.dtype, S.shape)
+        if out.numel() and out.data_ptr() == S.data_ptr():
+            raise ValueError("out must not be S")
+        _check(library().km_balance_grad(_ptr(S), _ptr(valid), _ptr(bal.counts), _ptr(bal.rows), _ptr(bal.lse),
+                                         _ptr(bal.dot), _ptr(grad), B, N, K, bal.picks, dt, _ptr(out), _stream(None)))
+    return out

@@ -18,6 +18,7 @@
 
 #include "../../include/km.h"
 #include "km_internal.h"
+#include "km_soft.h"
 
 namespace km {
 size_t assign_smem_for(int BN, int natoms, int XB, int CS, bool pair);
@@ -107,7 +108,7 @@ constexpr int kSmemLimit = 232448;  // 227 KB per block on sm_100
 
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
-uint64_t wait_limit_ns() {
+uint64_t wait_limit() {
   static uint64_t v = [] {
     const char* e = getenv("KM_WAIT_LIMIT_NS");
     uint64_t d = 2000000000ull;
@@ -129,19 +130,15 @@ int assign_form() {
   return v;
 }  // -1 = chosen by shape (pairs where BN >= 128)
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn get_encode() {
-  static EncodeTiledFn fn = nullptr;
+TensorMapEncoder get_encode() {
+  static TensorMapEncoder fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
         q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
+      fn = reinterpret_cast<TensorMapEncoder>(p);
   });
   return fn;
 }
@@ -151,7 +148,7 @@ EncodeTiledFn get_encode() {
 // rows/columns read as zero.
 int encode_map(CUtensorMap* m, const void* ptr, bool f32, int64_t inner, int64_t rows, int B, int box_rows,
                int swizzle_bytes = 128) {
-  EncodeTiledFn enc = get_encode();
+  TensorMapEncoder enc = get_encode();
   if (!enc) return fail(KM_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   const int es = f32 ? 4 : 2;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(B)};
@@ -199,6 +196,11 @@ int ceil_log2(int k) {
 namespace km {
 
 void set_last_error(const char* msg) { g_err = msg ? msg : ""; }
+
+int api_fail(int code, const char* msg) { return fail(code, "%s", msg); }
+int api_check_device() { return check_device(); }
+uint64_t api_wait_limit_ns() { return wait_limit(); }
+TensorMapEncoder tensor_map_encoder() { return get_encode(); }
 
 int make_plan(Plan& p, int op, int B, int64_t N, int D, int K, int dtype, int64_t chunk_rows, const char** why) {
   static thread_local char msg[256];
@@ -555,7 +557,7 @@ int km_assign(const void* X, const void* C, int B, int64_t N, int D, int K, int 
   if ((r = encode_aug_map(&camap, caug, f32, p.Kp, B, cbox(p))) != KM_OK) return r;
   double* tobj = at<double>(c.ws, p.off_tobj);
   int64_t groups = 0;
-  AssignArgs a{&xmap, &xamap, &cmap, &camap, B, N, K, p.Kp, idx, mindist, tobj, c.status(), wait_limit_ns(),
+  AssignArgs a{&xmap, &xamap, &cmap, &camap, B, N, K, p.Kp, idx, mindist, tobj, c.status(), wait_limit(),
                &groups};
   a.cop = clp;
   a.cop_row_bytes = op_row_bytes(p);
@@ -627,7 +629,7 @@ static int fit_impl(const void* X, const void* C0, int B, int64_t N, int D, int 
   int32_t* rk = p.small_update ? nullptr : at<int32_t>(c.ws, p.off_rk);
   for (int t = 0; t < iters; ++t) {
     int64_t groups = 0;
-    AssignArgs a{&xmap, &xamap, &cmap, &camap, B, N, K, p.Kp, idx, nullptr, tobj, c.status(), wait_limit_ns(),
+    AssignArgs a{&xmap, &xamap, &cmap, &camap, B, N, K, p.Kp, idx, nullptr, tobj, c.status(), wait_limit(),
                  &groups, clp, op_row_bytes(p)};
     if (ev && (per_phase || t == 0)) {
       KM_CUDA(cudaEventRecordWithFlags(ev[per_phase ? 3 * t : 0], c.s, rec_flags));
@@ -939,7 +941,7 @@ int fit_stream(const ChunkFn& chunk, bool slot_reuse, const void* C0, int64_t N,
         pc.ntiles = pc.tiles_per_inst;
         int64_t groups = 0;
         AssignArgs a{&xmap, &xamap, &cmap,      &camap,          1,       nr,  K,
-                     p.Kp,  idxc,   nullptr,    tobj,            c.status(), wait_limit_ns(), &groups,
+                     p.Kp,  idxc,   nullptr,    tobj,            c.status(), wait_limit(), &groups,
                      clp,   op_row_bytes(p)};
         KM_CUDA(launch_assign(pc, a, c.s));
         Ctx cc = c;

@@ -1,0 +1,115 @@
+// km_soft.h -- host-side declarations of the soft-assignment operators (8-bit
+// points, scores and their gradients, the balance loss) and what their
+// translation units share with km_api.cu.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace km {
+
+// ------------------------------------------------------ shared with km_api.cu
+// Sets the message km_last_error() returns and gives the status code back (a
+// CUDA failure that the host-side injector caused becomes KM_ERR_INJECTED).
+int api_fail(int code, const char* msg);
+// KM_OK on an sm_100 device, else the failure.
+int api_check_device();
+// Bound of every in-kernel wait (KM_WAIT_LIMIT_NS).
+uint64_t api_wait_limit_ns();
+// The driver's tensor-map encoder, looked up once (null if it has none).
+typedef CUresult (*TensorMapEncoder)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                     const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                     CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+TensorMapEncoder tensor_map_encoder();
+
+// ----------------------------------------------------------- 8-bit points
+// A row of D coordinates is q_ld(D) bytes of e4m3 (16-byte rows, which the
+// tensor maps need) and q_blocks(D) e8m0 scales, one per 128 coordinates.
+constexpr int kQBlock = 128;
+inline int64_t q_ld(int D) { return (static_cast<int64_t>(D) + 15) / 16 * 16; }
+inline int q_blocks(int D) { return (D + kQBlock - 1) / kQBlock; }
+
+cudaError_t launch_quantize(const void* X, int dtype, int64_t rows, int D, uint8_t* q, uint8_t* scale,
+                            cudaStream_t s);
+// Rows of ld_out elements are written (ld_out >= D; columns from D on are left).
+cudaError_t launch_dequantize(const uint8_t* q, const uint8_t* scale, int dtype, int64_t rows, int D, int64_t ld_out,
+                              void* X, cudaStream_t s);
+
+// ----------------------------------------------------------------- scores
+struct ScoresArgs {
+  const CUtensorMap* xmap;  // [B][N][D] e4m3, box 128 coordinates x 128 points
+  const CUtensorMap* cmap;  // [B][K][D] e4m3, box 128 coordinates x 128 centroids
+  const uint8_t* xs;
+  const uint8_t* cs;
+  const float* bias;  // [B][K] or null
+  float alpha;
+  int B;
+  int64_t N;
+  int D, K;
+  int dtype;
+  void* S;
+  unsigned int* status;
+  uint64_t limit_ns;
+};
+cudaError_t launch_scores(const ScoresArgs& a, cudaStream_t s);
+
+// ------------------------------------------------------------ score gradients
+// One product of the gradient: out[m][n] = alpha * sum_l A(m, l) * Bm[l][n],
+// A being the score gradients dS (planes bf16 matrices whose sum is dS), Bm
+// the operand the scores were taken from, in bf16 (exact for 8-bit points).
+struct GradMmArgs {
+  bool transposed;           // false: A(m, l) = dS[m][l] (dX); true: A(m, l) = dS[l][m] (dC)
+  const CUtensorMap* amap;   // [planes * B][N][K] bf16; box 64 x 128 rows, or 64 x 64 rows transposed
+  const CUtensorMap* bmap;   // [B][L][D] bf16, box 64 x 64 rows
+  int planes;
+  int B;
+  int64_t M;                 // rows of the output per instance
+  int64_t L;                 // length of the sum
+  int D;                     // columns of the output
+  int splits;                // pieces of the sum, each with its own output plane [split][B][M][D]
+  int64_t split_len;         // rows of the sum per piece (a multiple of 64)
+  float alpha;
+  int out_dtype;
+  void* out;
+  unsigned int* status;
+  uint64_t limit_ns;
+};
+cudaError_t launch_grad_mm(const GradMmArgs& a, cudaStream_t s);
+// Width of the output tile launch_grad_mm uses for D columns.
+int grad_mm_tile(int D);
+// out[i] = sum over splits of part[split][i], in split order.
+cudaError_t launch_split_sum(const float* part, int splits, int64_t n, float* out, cudaStream_t s);
+// dS (dtype) as 1 (bf16) or 3 (f32) bf16 planes [planes][rows][ld]; the planes sum to dS
+// exactly for values whose third piece does not underflow.
+cudaError_t launch_split_planes(const void* dS, int dtype, int64_t rows, int K, int64_t ld, void* planes,
+                                cudaStream_t s);
+// dbias[b][k] = sum_i dS[b][i][k] through part [B][chunks][K].
+int64_t colsum_chunks(int B, int64_t N, int K);
+cudaError_t launch_colsum(const void* dS, int dtype, int B, int64_t N, int K, float* part, float* dbias,
+                          cudaStream_t s);
+
+// ---------------------------------------------------------------- balance
+struct BalanceArgs {
+  const void* S;
+  const int32_t* idx;
+  const uint8_t* valid;  // or null
+  int B;
+  int64_t N;
+  int K, T, dtype;
+  float* loss;
+  int32_t* counts;
+  int32_t* rows;
+  float* lse;
+  float* dot;
+  double* part;  // [B][balance_blocks]
+  // gradient only
+  const float* grad;  // [B] or null (1)
+  void* dS;
+};
+int balance_blocks(int B, int64_t N);
+cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t s);
+cudaError_t launch_balance_grad(const BalanceArgs& a, cudaStream_t s);
+
+}  // namespace km
