@@ -8,11 +8,24 @@
 // pieces whose products are accumulated together (three times 8 significant
 // bits hold the 24 of a float32).
 //
-// k_grad_mm is one product of a bf16 matrix chain, 128 x BN tiles, tcgen05
-// MMAs with both operands staged by TMA (128-byte swizzle) in slices of 64
-// terms of the sum.  dX reads dS as it lies (the sum runs along its rows); dC
-// sums over the points, so both of its operands are MN-major: the slices are
-// 64 points x 64 columns, and the MMA transposes them as it reads.
+// dS is by far the largest operand and both products need all of it, so one
+// kernel takes both: a group of CTAs, one per 256 centroids, walks a range of
+// points; in each step every CTA first forms dX of 256 points of its own
+// (their dS rows come from HBM), then adds the points of the whole group's
+// step to its 256 centroids' dC (those dS columns were just read by the
+// group's CTAs, and come from L2).  HBM sees dS once.
+//
+// Both products are taken transposed, D along the MMA's M (128) and points or
+// centroids along its N (256): the widest tile one CTA can issue, 12 KB of
+// shared memory read per 16-term step instead of the 16 KB that two 128-wide
+// tiles would read.  A lane of the accumulator is then one coordinate, and
+// the epilogue's stores run along the coordinates of a row with no staging.
+// Both accumulators (256 columns each) stay in tensor memory side by side, so
+// that dX's epilogue runs under dC's MMAs.
+//
+// Structure: warp 0 TMA, warp 1 MMA, warps 2..9 epilogue, warps 10..17 column
+// sums (dbias, from the staged dS slices of the dC product: float32 over 16
+// points, those joined in float64).  Every wait is bounded in time.
 #include "km_internal.h"
 #include "km_soft.h"
 #include "km_tile.cuh"
@@ -21,50 +34,48 @@ namespace km {
 
 namespace {
 
-constexpr int kThreads = 320;  // warp 0 TMA, warp 1 MMA, warps 2..9 epilogue
-constexpr int kBM = 128;
-constexpr int kSlice = 64;     // terms of the sum per stage
-constexpr int kABytes = kBM * kSlice * 2;
+constexpr int kThreads = 576;
+constexpr int kDT = 128;       // coordinates per tile (MMA M)
+constexpr int kRT = 256;       // points per dX tile (MMA N)
+constexpr int kSlice = 64;     // terms of a sum per stage
+constexpr int kABytes = kDT * kSlice * 2;
+constexpr int kBBytes = kRT * kSlice * 2;
 constexpr int kBoxBytes = kSlice * 64 * 2;  // 64 terms x 64 columns
-
-template <int BN>
-__host__ __device__ constexpr int stage_bytes() { return kABytes + BN / 64 * kBoxBytes; }
-template <int BN>
-__host__ __device__ constexpr int stages() { return BN == 64 ? 6 : (BN == 128 ? 5 : 3); }
-template <int BN>
-constexpr size_t smem_bytes() { return 1024 + stages<BN>() * stage_bytes<BN>() + 8 * kStageBytes + 32 * 8; }
+constexpr int kStageB = kABytes + kBBytes;
+constexpr int kStages = 4;
+constexpr int kEpiWarps = 8, kSumWarps = 8;
+constexpr uint32_t kTmemCols = 512;
+constexpr size_t kSmem = 1024 + kStages * kStageB + 32 * 8;
 
 struct GradK {
-  int planes, B, D;
-  int64_t M, L, split_len;
-  int splits;
-  int64_t mt, nt, ntiles;
+  int planes, B, D, K;
+  int64_t N;
+  int64_t tpi;         // 256-point tiles per instance
+  int nkt, group, passes;  // centroid tiles, CTAs per group, centroid tiles per CTA
+  int splits, ndt;
+  int64_t items, groups;
   float alpha;
-  void* out;
-  bool vec;
+  void* dX;
+  float* dC;           // [splits][B][K][D]
+  float* db;           // [splits * parts][B][K]
   unsigned int* status;
   uint64_t limit_ns;
 };
 
-struct Item {
-  int b, split, n0;
-  int64_t m0, l0, l1;
+// The walk of a CTA, the same in every role: items (instance, split of its
+// points, 128-coordinate tile), passes over its centroid tiles, steps.
+struct Walk {
+  int b, split, dt;
+  int64_t t0, t1;  // 256-point tiles
+  __device__ __forceinline__ Walk(int64_t item, const GradK& p) {
+    dt = static_cast<int>(item % p.ndt);
+    const int64_t r = item / p.ndt;
+    split = static_cast<int>(r % p.splits);
+    b = static_cast<int>(r / p.splits);
+    t0 = split * p.tpi / p.splits;
+    t1 = (split + 1) * p.tpi / p.splits;
+  }
 };
-__device__ __forceinline__ Item item_at(int64_t t, const GradK& p, int BN) {
-  Item it;
-  const int64_t n = t % p.nt;
-  int64_t r = t / p.nt;
-  const int64_t m = r % p.mt;
-  r /= p.mt;
-  const int64_t sp = r % p.splits;
-  it.b = static_cast<int>(r / p.splits);
-  it.split = static_cast<int>(sp);
-  it.n0 = static_cast<int>(n) * BN;
-  it.m0 = m * kBM;
-  it.l0 = sp * p.split_len;
-  it.l1 = it.l0 + p.split_len < p.L ? it.l0 + p.split_len : p.L;
-  return it;
-}
 
 // MN-major operand with the 128-byte swizzle: 64 columns (128 bytes) by 8
 // terms per core matrix, 1024 bytes to the next 8 terms (stride byte offset),
@@ -79,40 +90,41 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
   return d;
 }
 
-// TR: A(m, l) = dS[l][m].
-template <int BN, bool TR, bool OUT_BF16>
+// KT centroids per dC tile (the MMA's N).
+template <int KT, bool OUT_BF16, bool WX, bool WC, bool WB>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_grad_mm(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const GradK p) {
+    k_grad(const __grid_constant__ CUtensorMap ds_x, const __grid_constant__ CUtensorMap ds_c,
+           const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CUtensorMap xmap, const GradK p) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  constexpr int ST = stages<BN>(), SB = stage_bytes<BN>();
-  uint8_t* ops = base;
-  uint8_t* staging = ops + ST * SB;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + 8 * kStageBytes);
-  uint64_t* full = bars;        // [ST]
-  uint64_t* empty = bars + 8;   // [ST]
-  uint64_t* a_full = bars + 16;   // [2]
-  uint64_t* a_empty = bars + 18;  // [2]
-  uint64_t* drain = bars + 20;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 21);
+  uint8_t* ops = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ops + kStages * kStageB);
+  uint64_t* full = bars;        // [kStages]
+  uint64_t* empty = bars + 4;   // [kStages]
+  uint64_t* x_full = bars + 8;
+  uint64_t* x_empty = bars + 9;
+  uint64_t* c_full = bars + 10;
+  uint64_t* c_empty = bars + 11;
+  uint64_t* drain = bars + 12;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 13);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr bool kRows = WC || WB;  // the second product (or its column sums) is wanted
   if (threadIdx.x == 0) {
-    for (int i = 0; i < ST; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], 1 + (WB ? kSumWarps : 0));
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&a_full[i], 1);
-      mbar_init(&a_empty[i], 4);
-    }
+    mbar_init(x_full, 1);
+    mbar_init(x_empty, kEpiWarps);
+    mbar_init(c_full, 1);
+    mbar_init(c_empty, kEpiWarps);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_holder, 2 * BN);
+    tmem_alloc(tmem_holder, kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -120,36 +132,65 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const WaitGuard g{p.status, abort_flag, p.limit_ns};
+  const int64_t grp = blockIdx.x / p.group;
+  const int me = static_cast<int>(blockIdx.x - grp * p.group);
+  const int kslices = (p.K + kSlice - 1) / kSlice;
+  // point slices of the step starting at tile t
+  auto step_slices = [&](int64_t t, int64_t t1) {
+    const int64_t r0 = t * kRT, e = (t + p.group < t1 ? t + p.group : t1) * kRT;
+    return static_cast<int>(((e < p.N ? e : p.N) - r0 + kSlice - 1) / kSlice);
+  };
 
   if (warp == 0) {
     if (lane == 0) {
-      prefetch_tensormap(&amap);
-      prefetch_tensormap(&bmap);
+      prefetch_tensormap(&ds_x);
+      prefetch_tensormap(&ds_c);
+      prefetch_tensormap(&cmap);
+      prefetch_tensormap(&xmap);
       int st = 0;
       uint32_t ph = 0;
-      int issued[ST];
+      int issued[kStages];
 #pragma unroll
-      for (int i = 0; i < ST; ++i) issued[i] = -1;
+      for (int i = 0; i < kStages; ++i) issued[i] = -1;
       bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < p.ntiles; t += gridDim.x) {
-        const Item it = item_at(t, p, BN);
-        for (int64_t l = it.l0; ok && l < it.l1; l += kSlice) {
-          for (int pl = 0; pl < p.planes; ++pl) {
-            if (!mbar_wait(&empty[st], ph ^ 1u, g)) { ok = false; break; }
-            uint8_t* dst = ops + st * SB;
-            mbar_arrive_expect_tx(&full[st], SB);
-            const int z = pl * p.B + it.b;
-            if constexpr (TR) {
-              tma_load_3d(dst, &amap, static_cast<int>(it.m0), static_cast<int>(l), z, &full[st]);
-              tma_load_3d(dst + kBoxBytes, &amap, static_cast<int>(it.m0) + 64, static_cast<int>(l), z, &full[st]);
-            } else {
-              tma_load_3d(dst, &amap, static_cast<int>(l), static_cast<int>(it.m0), z, &full[st]);
+      auto next = [&]() { if (++st == kStages) { st = 0; ph ^= 1u; } };
+      for (int64_t item = grp; ok && item < p.items; item += p.groups) {
+        const Walk w(item, p);
+        const int d0 = w.dt * kDT;
+        for (int ps = 0; ok && ps < p.passes; ++ps) {
+          const int kt = ps * p.group + me;
+          for (int64_t t = w.t0; ok && t < w.t1; t += p.group) {
+            if (WX && ps == 0 && t + me < w.t1) {
+              const int r0 = static_cast<int>((t + me) * kRT);
+              for (int i = 0; ok && i < kslices * p.planes; ++i) {
+                const int l = i / p.planes, pl = i - l * p.planes;
+                if (!mbar_wait(&empty[st], ph ^ 1u, g)) { ok = false; break; }
+                uint8_t* dst = ops + st * kStageB;
+                mbar_arrive_expect_tx(&full[st], kStageB);
+                tma_load_3d(dst, &cmap, d0, l * kSlice, w.b, &full[st]);
+                tma_load_3d(dst + kBoxBytes, &cmap, d0 + 64, l * kSlice, w.b, &full[st]);
+                tma_load_3d(dst + kABytes, &ds_x, l * kSlice, r0, pl * p.B + w.b, &full[st]);
+                issued[st] = static_cast<int>(ph);
+                next();
+              }
             }
+            if (kRows && kt < p.nkt && ok) {
+              const int n = step_slices(t, w.t1) * p.planes;
+              for (int i = 0; i < n; ++i) {
+                const int l = i / p.planes, pl = i - l * p.planes;
+                const int r0 = static_cast<int>(t * kRT + l * kSlice);
+                if (!mbar_wait(&empty[st], ph ^ 1u, g)) { ok = false; break; }
+                uint8_t* dst = ops + st * kStageB;
+                mbar_arrive_expect_tx(&full[st], kABytes + KT / 64 * kBoxBytes);
+                tma_load_3d(dst, &xmap, d0, r0, w.b, &full[st]);
+                tma_load_3d(dst + kBoxBytes, &xmap, d0 + 64, r0, w.b, &full[st]);
 #pragma unroll
-            for (int j = 0; j < BN / 64; ++j)
-              tma_load_3d(dst + kABytes + j * kBoxBytes, &bmap, it.n0 + j * 64, static_cast<int>(l), it.b, &full[st]);
-            issued[st] = static_cast<int>(ph);
-            if (++st == ST) { st = 0; ph ^= 1u; }
+                for (int j = 0; j < KT / 64; ++j)
+                  tma_load_3d(dst + kABytes + j * kBoxBytes, &ds_c, kt * KT + j * 64, r0, pl * p.B + w.b, &full[st]);
+                issued[st] = static_cast<int>(ph);
+                next();
+              }
+            }
           }
         }
       }
@@ -158,37 +199,70 @@ __global__ void __launch_bounds__(kThreads, 1)
       volatile int never = 0;
       WaitGuard g2 = g;
       g2.abort_flag = &never;
-      for (int i = 0; i < ST; ++i)
+      for (int i = 0; i < kStages; ++i)
         if (issued[i] >= 0) mbar_wait(&full[i], static_cast<uint32_t>(issued[i]), g2);
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      // bf16 x bf16 -> f32; bit 16: B is MN-major, bit 15: so is A
-      constexpr uint32_t idesc = umma_idesc(false, kBM, BN) | (1u << 16) | (TR ? 1u << 15 : 0u);
-      int st = 0, ab = 0;
-      uint32_t ph = 0, aph = 0;
+      // bf16 x bf16 -> f32; bit 15: A is MN-major, bit 16: so is B (dC)
+      constexpr uint32_t idesc_x = umma_idesc(false, kDT, kRT) | (1u << 15);
+      constexpr uint32_t idesc_c = umma_idesc(false, kDT, KT) | (1u << 15) | (1u << 16);
+      int st = 0;
+      uint32_t ph = 0, xph = 0, cph = 0;
       bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < p.ntiles; t += gridDim.x) {
-        const Item it = item_at(t, p, BN);
-        if (!mbar_wait(&a_empty[ab], aph ^ 1u, g)) break;
-        const uint32_t d = tmem + static_cast<uint32_t>(ab * BN);
-        const int64_t slices = (it.l1 - it.l0 + kSlice - 1) / kSlice * p.planes;
-        for (int64_t i = 0; i < slices; ++i) {
-          if (!mbar_wait(&full[st], ph, g)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t a = smem_addr(ops + st * SB);
-#pragma unroll
-          for (int s = 0; s < kSlice / 16; ++s) {
-            const uint64_t ad = TR ? sw128_mnmajor_desc(a + s * 2048) : sw128_kmajor_desc(a + s * 32);
-            umma_ss<false>(d, ad, sw128_mnmajor_desc(a + kABytes + s * 2048), idesc, i != 0 || s != 0 ? 1u : 0u);
+      auto next = [&]() { if (++st == kStages) { st = 0; ph ^= 1u; } };
+      for (int64_t item = grp; ok && item < p.items; item += p.groups) {
+        const Walk w(item, p);
+        for (int ps = 0; ok && ps < p.passes; ++ps) {
+          const int kt = ps * p.group + me;
+          const bool rows = kRows && kt < p.nkt;
+          uint32_t acc_c = 0;
+          if (rows) {
+            if (!mbar_wait(c_empty, cph ^ 1u, g)) { ok = false; break; }
           }
-          umma_commit(&empty[st]);
-          if (++st == ST) { st = 0; ph ^= 1u; }
+          for (int64_t t = w.t0; ok && t < w.t1; t += p.group) {
+            if (WX && ps == 0 && t + me < w.t1) {
+              if (!mbar_wait(x_empty, xph ^ 1u, g)) { ok = false; break; }
+              for (int i = 0; i < kslices * p.planes; ++i) {
+                if (!mbar_wait(&full[st], ph, g)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t a = smem_addr(ops + st * kStageB);
+#pragma unroll
+                for (int s = 0; s < kSlice / 16; ++s)
+                  umma_ss<false>(tmem, sw128_mnmajor_desc(a + s * 2048), sw128_kmajor_desc(a + kABytes + s * 32), idesc_x,
+                                 i != 0 || s != 0 ? 1u : 0u);
+                umma_commit(&empty[st]);
+                next();
+              }
+              if (!ok) break;
+              umma_commit(x_full);
+              xph ^= 1u;
+            }
+            if (rows) {
+              const int n = step_slices(t, w.t1) * p.planes;
+              for (int i = 0; i < n; ++i) {
+                if (!mbar_wait(&full[st], ph, g)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t a = smem_addr(ops + st * kStageB);
+                if (WC) {
+#pragma unroll
+                  for (int s = 0; s < kSlice / 16; ++s) {
+                    umma_ss<false>(tmem + kRT, sw128_mnmajor_desc(a + s * 2048),
+                                   sw128_mnmajor_desc(a + kABytes + s * 2048), idesc_c, acc_c);
+                    acc_c = 1;
+                  }
+                }
+                umma_commit(&empty[st]);
+                next();
+              }
+            }
+          }
+          if (!ok) break;
+          if (rows) {
+            umma_commit(c_full);
+            cph ^= 1u;
+          }
         }
-        if (!ok) break;
-        umma_commit(&a_full[ab]);
-        ab ^= 1;
-        if (ab == 0) aph ^= 1u;
       }
       umma_commit(drain);  // every MMA is done before TMEM can be released
       volatile int never = 0;
@@ -196,48 +270,119 @@ __global__ void __launch_bounds__(kThreads, 1)
       g2.abort_flag = &never;
       mbar_wait(drain, 0u, g2);
     }
-  } else {
-    const int q = warp & 3, grp = (warp - 2) >> 2;
-    const uint32_t col0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(grp * BN);
-    uint8_t* stage = staging + (warp - 2) * kStageBytes;
-    constexpr int ES = OUT_BF16 ? 2 : 4;
-    constexpr int kCols = 128 / ES;
-    const int64_t row_bytes = static_cast<int64_t>(p.D) * ES;
-    uint32_t aph = 0;
-    int64_t seq = 0;
-    for (int64_t t = blockIdx.x; t < p.ntiles; t += gridDim.x, ++seq) {
-      if ((seq & 1) != grp) continue;
-      const Item it = item_at(t, p, BN);
-      const int64_t m = it.m0 + q * 32;
-      const int rows = static_cast<int>(m + 32 <= p.M ? 32 : (p.M > m ? p.M - m : 0));
-      uint8_t* out = static_cast<uint8_t*>(p.out) +
-                     ((static_cast<int64_t>(it.split) * p.B + it.b) * p.M + m) * row_bytes +
-                     static_cast<int64_t>(it.n0) * ES;
-      const int ncol = p.D - it.n0 < BN ? p.D - it.n0 : BN;
-      if (!__all_sync(0xffffffffu, mbar_wait(&a_full[grp], aph, g))) break;
-      aph ^= 1u;
-      tc_fence_after();
+  } else if (warp < 2 + kEpiWarps) {
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
+    uint32_t xph = 0, cph = 0;
+    bool ok = true;
+    // cols columns of an accumulator from col on, this lane's coordinate of each, to row r of out
+    auto drain_cols = [&](uint32_t col, int64_t n, int d, auto* out, uint64_t* done) {
+      n = n < 0 ? 0 : n;
 #pragma unroll 1
-      for (int c = 0; c < BN / 32; ++c) {
+      for (int c = 0; c < 4; ++c) {
         uint32_t r[32];
-        tmem_load32(col0 + static_cast<uint32_t>(c * 32), r);
+        tmem_load32(tmem + lane_off + col + static_cast<uint32_t>(c * 32), r);
         tmem_wait32(r);
-        if (c == BN / 32 - 1) {
+        if (c == 3) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&a_empty[grp]);
+          if (lane == 0) mbar_arrive(done);
         }
-        float v[32];
+        if (d < p.D) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * p.alpha;
-        const int c0 = OUT_BF16 ? (c & ~1) * 32 : c * 32;
-        if constexpr (OUT_BF16) stage_bf16(stage, v, c & 1, lane);
-        else stage_f32(stage, v, lane);
-        if (!OUT_BF16 || (c & 1)) {
-          __syncwarp();
-          const int n = ncol - c0 < kCols ? ncol - c0 : kCols;
-          if (n > 0) store_staged<ES>(stage, out + c0 * ES, row_bytes, rows, n * ES, p.vec, lane);
-          __syncwarp();
+          for (int i = 0; i < 32; ++i) {
+            if (c * 32 + i >= n) break;
+            const float v = __uint_as_float(r[i]) * p.alpha;
+            auto* o = out + static_cast<int64_t>(c * 32 + i) * p.D + d;
+            if constexpr (sizeof(*o) == 2) *o = __float2bfloat16_rn(v);
+            else *o = v;
+          }
+        }
+      }
+    };
+    using XT = typename std::conditional<OUT_BF16, __nv_bfloat16, float>::type;
+    for (int64_t item = grp; ok && item < p.items; item += p.groups) {
+      const Walk w(item, p);
+      const int d = w.dt * kDT + q * 32 + lane;
+      for (int ps = 0; ok && ps < p.passes; ++ps) {
+        const int kt = ps * p.group + me;
+        if (WX && ps == 0) {
+          for (int64_t t = w.t0 + me; t < w.t1; t += p.group) {
+            if (!__all_sync(0xffffffffu, mbar_wait(x_full, xph, g))) { ok = false; break; }
+            xph ^= 1u;
+            tc_fence_after();
+            const int64_t r0 = t * kRT + half * 128;
+            drain_cols(static_cast<uint32_t>(half * 128), p.N - r0, d,
+                       static_cast<XT*>(p.dX) + (static_cast<int64_t>(w.b) * p.N + r0) * p.D, x_empty);
+          }
+        }
+        if (!ok) break;
+        if (kRows && kt < p.nkt) {
+          if (!__all_sync(0xffffffffu, mbar_wait(c_full, cph, g))) { ok = false; break; }
+          cph ^= 1u;
+          tc_fence_after();
+          const int k0 = kt * KT + half * 128;
+          const int64_t n = WC && half * 128 < KT ? (p.K - k0 < KT - half * 128 ? p.K - k0 : KT - half * 128) : 0;
+          drain_cols(static_cast<uint32_t>(kRT + half * 128), n, d,
+                     p.dC + ((static_cast<int64_t>(w.split) * p.B + w.b) * p.K + k0) * p.D, c_empty);
+        }
+      }
+    }
+  } else if (WB) {
+    // column sums: each warp sums its share of a slice's points for 64 centroids, two per lane
+    constexpr int kParts = kSumWarps / (KT / 64);  // warps that share 64 centroids
+    constexpr int kN = kSlice / kParts;            // points of a slice per warp
+    const int cw = warp - 2 - kEpiWarps, box = cw / kParts, part = cw % kParts;
+    int st = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    auto next = [&]() { if (++st == kStages) { st = 0; ph ^= 1u; } };
+    for (int64_t item = grp; ok && item < p.items; item += p.groups) {
+      const Walk w(item, p);
+      for (int ps = 0; ok && ps < p.passes; ++ps) {
+        const int kt = ps * p.group + me;
+        double a0 = 0.0, a1 = 0.0;
+        for (int64_t t = w.t0; ok && t < w.t1; t += p.group) {
+          const int nx = WX && ps == 0 && t + me < w.t1 ? kslices * p.planes : 0;
+          for (int i = 0; i < nx; ++i) {  // dX's slices: not looked at
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[st], ph, g))) { ok = false; break; }
+            if (lane == 0) mbar_arrive(&empty[st]);
+            next();
+          }
+          if (!ok) break;
+          if (kt < p.nkt) {
+            const int n = step_slices(t, w.t1) * p.planes;
+            for (int i = 0; i < n; ++i) {
+              if (!__all_sync(0xffffffffu, mbar_wait(&full[st], ph, g))) { ok = false; break; }
+              const uint8_t* bx = ops + st * kStageB + kABytes + box * kBoxBytes;
+              if (w.dt == 0) {
+#pragma unroll
+                for (int h = 0; h < kN; h += 16) {
+                  float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                  for (int j = 0; j < (kN < 16 ? kN : 16); ++j) {
+                    const int r = part * kN + h + j;
+                    const uint32_t v = *reinterpret_cast<const uint32_t*>(
+                        bx + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2)));
+                    s0 += __uint_as_float(v << 16);
+                    s1 += __uint_as_float(v & 0xffff0000u);
+                  }
+                  a0 += s0;
+                  a1 += s1;
+                }
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&empty[st]);
+              next();
+            }
+          }
+        }
+        if (!ok) break;
+        if (w.dt == 0 && kt < p.nkt) {
+          const int k = kt * KT + box * 64 + lane * 2;
+          float* o = p.db + (static_cast<int64_t>(w.split * kParts + part) * p.B + w.b) * p.K;
+          if (k < p.K) o[k] = static_cast<float>(a0);
+          if (k + 1 < p.K) o[k + 1] = static_cast<float>(a1);
         }
       }
     }
@@ -245,39 +390,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 2 * BN);
+    tmem_dealloc(tmem, kTmemCols);
   }
-}
-
-template <int BN, bool TR, bool OUT_BF16>
-cudaError_t grad_mm_t(const GradMmArgs& a, const GradK& k, int nsm, cudaStream_t s) {
-  auto kern = k_grad_mm<BN, TR, OUT_BF16>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem_bytes<BN>()));
-  if (e != cudaSuccess) return e;
-  chain_break();
-  if (fault_hit(kFaultLaunch)) return cudaErrorLaunchFailure;
-  count_launch();
-  kern<<<static_cast<unsigned>(k.ntiles < nsm ? k.ntiles : nsm), kThreads, smem_bytes<BN>(), s>>>(*a.amap, *a.bmap, k);
-  return cudaGetLastError();
-}
-
-template <int BN>
-cudaError_t grad_mm_bn(const GradMmArgs& a, const GradK& k, int nsm, cudaStream_t s) {
-  if (a.transposed) return grad_mm_t<BN, true, false>(a, k, nsm, s);
-  return a.out_dtype == kDtypeBF16 ? grad_mm_t<BN, false, true>(a, k, nsm, s) : grad_mm_t<BN, false, false>(a, k, nsm, s);
 }
 
 // ------------------------------------------------------------ small kernels
 constexpr int kT = 256;
 
-__global__ void __launch_bounds__(kT) k_split_sum(const float* __restrict__ part, int splits, int64_t n,
-                                                  float* __restrict__ out) {
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kT + threadIdx.x; i < n;
+// out[i] = sum over the pieces, in order, for dC (nc elements) and dbias (nb).
+__global__ void __launch_bounds__(kT) k_grad_join(const float* __restrict__ cpart, int csplits, int64_t nc,
+                                                  float* __restrict__ dC, const float* __restrict__ bpart, int bsplits,
+                                                  int64_t nb, float* __restrict__ dbias) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kT + threadIdx.x; i < nc + nb;
        i += static_cast<int64_t>(gridDim.x) * kT) {
-    float v = 0.f;
-    for (int s = 0; s < splits; ++s) v += part[static_cast<int64_t>(s) * n + i];
-    out[i] = v;
+    if (i < nc) {
+      float v = 0.f;
+      for (int s = 0; s < csplits; ++s) v += cpart[static_cast<int64_t>(s) * nc + i];
+      dC[i] = v;
+    } else {
+      double v = 0.0;
+      for (int s = 0; s < bsplits; ++s) v += bpart[static_cast<int64_t>(s) * nb + i - nc];
+      dbias[i - nc] = static_cast<float>(v);
+    }
   }
 }
 
@@ -303,42 +437,6 @@ __global__ void __launch_bounds__(kT) k_split_planes(const void* __restrict__ dS
   }
 }
 
-// Column sums of a chunk of rows: a thread per column, float32 over 16 rows,
-// those joined in float64.
-template <bool BF16>
-__global__ void __launch_bounds__(128) k_colsum(const void* __restrict__ dS, int64_t N, int K, int64_t chunk,
-                                                int64_t chunks, float* __restrict__ part) {
-  const int64_t cols = (K + 127) / 128;  // blocks of columns, then chunks, then instances
-  const int64_t bc = blockIdx.x / cols, b = bc / chunks, ch = bc - b * chunks;
-  const int c = static_cast<int>(blockIdx.x - bc * cols) * 128 + threadIdx.x;
-  if (c >= K) return;
-  const int64_t i0 = ch * chunk;
-  const int64_t i1 = i0 + chunk < N ? i0 + chunk : N;
-  double acc = 0.0;
-  for (int64_t i = i0; i < i1; i += 16) {
-    float v = 0.f;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      if (i + j >= i1) break;
-      const int64_t o = (b * N + i + j) * K + c;
-      v += BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(dS)[o]) : static_cast<const float*>(dS)[o];
-    }
-    acc += v;
-  }
-  part[bc * K + c] = static_cast<float>(acc);
-}
-
-__global__ void __launch_bounds__(kT) k_colsum_join(const float* __restrict__ part, int64_t chunks, int64_t n, int K,
-                                                    float* __restrict__ out) {
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kT + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * kT) {
-    const int64_t b = i / K, c = i - b * K;
-    double v = 0.0;
-    for (int64_t j = 0; j < chunks; ++j) v += part[(b * chunks + j) * K + c];
-    out[i] = static_cast<float>(v);
-  }
-}
-
 unsigned grid_of(int64_t n) {
   const int64_t b = (n + kT - 1) / kT;
   return static_cast<unsigned>(b < 148 * 16 ? b : 148 * 16);
@@ -351,44 +449,99 @@ cudaError_t plain_launch() {
   return cudaSuccess;
 }
 
+template <int KT, bool OUT_BF16, bool WX, bool WC, bool WB>
+cudaError_t grad_t(const GradArgs& a, const GradK& k, cudaStream_t s) {
+  auto kern = k_grad<KT, OUT_BF16, WX, WC, WB>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+  if (e != cudaSuccess) return e;
+  if ((e = plain_launch()) != cudaSuccess) return e;
+  kern<<<static_cast<unsigned>(k.groups * k.group), kThreads, kSmem, s>>>(*a.ds_x, *a.ds_c, *a.cmap, *a.xmap, k);
+  return cudaGetLastError();
+}
+
+template <int KT, bool OUT_BF16>
+cudaError_t grad_w(const GradArgs& a, const GradK& k, cudaStream_t s) {
+  const int w = (a.dX ? 4 : 0) + (a.dC ? 2 : 0) + (a.db ? 1 : 0);
+  switch (w) {
+    case 7: return grad_t<KT, OUT_BF16, true, true, true>(a, k, s);
+    case 6: return grad_t<KT, OUT_BF16, true, true, false>(a, k, s);
+    case 5: return grad_t<KT, OUT_BF16, true, false, true>(a, k, s);
+    case 4: return grad_t<KT, OUT_BF16, true, false, false>(a, k, s);
+    case 3: return grad_t<KT, OUT_BF16, false, true, true>(a, k, s);
+    case 2: return grad_t<KT, OUT_BF16, false, true, false>(a, k, s);
+    default: return grad_t<KT, OUT_BF16, false, false, true>(a, k, s);
+  }
+}
+
+template <int KT>
+cudaError_t grad_k(const GradArgs& a, const GradK& k, cudaStream_t s) {
+  return a.dX && a.dx_dtype == kDtypeBF16 ? grad_w<KT, true>(a, k, s) : grad_w<KT, false>(a, k, s);
+}
+
 }  // namespace
 
-int grad_mm_tile(int D) { return D <= 64 ? 64 : (D <= 128 ? 128 : 256); }
+GradPlan grad_plan(int B, int64_t N, int D, int K) {
+  GradPlan pl{};
+  pl.kt = K <= 64 ? 64 : (K <= 128 ? 128 : 256);
+  pl.nkt = (K + pl.kt - 1) / pl.kt;
+  pl.group = pl.nkt < kGradCtas ? pl.nkt : kGradCtas;
+  pl.passes = (pl.nkt + pl.group - 1) / pl.group;
+  const int ndt = (D + kDT - 1) / kDT;
+  const int64_t tpi = (N + kRT - 1) / kRT;
+  const int64_t groups = kGradCtas / pl.group;
+  // Pieces of an instance's points, each with its own dC: as few as let the
+  // groups finish together (rounds of items times steps of an item).
+  int64_t best = -1;
+  pl.splits = 1;
+  for (int64_t sp = 1; sp <= groups && sp <= (tpi > 1 ? tpi : 1); ++sp) {
+    const int64_t rounds = (static_cast<int64_t>(B) * sp * ndt + groups - 1) / groups;
+    const int64_t per = (tpi + sp - 1) / sp;
+    const int64_t cost = rounds * ((per + pl.group - 1) / pl.group);
+    if (best < 0 || cost < best) {
+      best = cost;
+      pl.splits = static_cast<int>(sp);
+    }
+  }
+  pl.parts = kSumWarps / (pl.kt / 64);
+  const int64_t items = static_cast<int64_t>(B) * pl.splits * ndt;
+  pl.groups = items < groups ? items : groups;
+  return pl;
+}
 
-cudaError_t launch_grad_mm(const GradMmArgs& a, cudaStream_t s) {
-  const int BN = grad_mm_tile(a.D);
+cudaError_t launch_grad(const GradArgs& a, cudaStream_t s) {
+  const GradPlan pl = grad_plan(a.B, a.N, a.D, a.K);
   GradK k{};
   k.planes = a.planes;
   k.B = a.B;
   k.D = a.D;
-  k.M = a.M;
-  k.L = a.L;
-  k.split_len = a.split_len;
-  k.splits = a.splits;
-  k.mt = (a.M + kBM - 1) / kBM;
-  k.nt = (a.D + BN - 1) / BN;
-  k.ntiles = k.mt * k.nt * a.splits * a.B;
+  k.K = a.K;
+  k.N = a.N;
+  k.tpi = (a.N + kRT - 1) / kRT;
+  k.nkt = pl.nkt;
+  k.group = pl.group;
+  k.passes = a.dC || a.db ? pl.passes : 1;
+  k.splits = pl.splits;
+  k.ndt = a.dX || a.dC ? (a.D + kDT - 1) / kDT : 1;
+  k.items = static_cast<int64_t>(a.B) * pl.splits * k.ndt;
+  k.groups = pl.groups < k.items ? pl.groups : k.items;
   k.alpha = a.alpha;
-  k.out = a.out;
-  const int es = a.out_dtype == kDtypeBF16 ? 2 : 4;
-  k.vec = static_cast<int64_t>(a.D) * es % 16 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
+  k.dX = a.dX;
+  k.dC = a.dC;
+  k.db = a.db;
   k.status = a.status;
   k.limit_ns = a.limit_ns;
-  if (k.ntiles == 0) return cudaSuccess;
-  int dev = 0, nsm = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
-  switch (BN) {
-    case 64: return grad_mm_bn<64>(a, k, nsm, s);
-    case 128: return grad_mm_bn<128>(a, k, nsm, s);
-    default: return grad_mm_bn<256>(a, k, nsm, s);
+  switch (pl.kt) {
+    case 64: return grad_k<64>(a, k, s);
+    case 128: return grad_k<128>(a, k, s);
+    default: return grad_k<256>(a, k, s);
   }
 }
 
-cudaError_t launch_split_sum(const float* part, int splits, int64_t n, float* out, cudaStream_t s) {
+cudaError_t launch_grad_join(const float* cpart, int csplits, int64_t nc, float* dC, const float* bpart, int bsplits,
+                             int64_t nb, float* dbias, cudaStream_t s) {
   cudaError_t e = plain_launch();
   if (e != cudaSuccess) return e;
-  k_split_sum<<<grid_of(n), kT, 0, s>>>(part, splits, n, out);
+  k_grad_join<<<grid_of(nc + nb), kT, 0, s>>>(cpart, csplits, nc, dC, bpart, bsplits, nb, dbias);
   return cudaGetLastError();
 }
 
@@ -399,32 +552,6 @@ cudaError_t launch_split_planes(const void* dS, int dtype, int64_t rows, int K, 
   auto* o = static_cast<__nv_bfloat16*>(planes);
   if (dtype == kDtypeBF16) k_split_planes<true><<<grid_of(rows * K), kT, 0, s>>>(dS, rows * K, K, ld, rows * ld, o);
   else k_split_planes<false><<<grid_of(rows * K), kT, 0, s>>>(dS, rows * K, K, ld, rows * ld, o);
-  return cudaGetLastError();
-}
-
-int64_t colsum_chunks(int B, int64_t N, int K) {
-  const int64_t per = static_cast<int64_t>(B) * ((K + 127) / 128);
-  int64_t c = (148 * 16 + per - 1) / per;
-  const int64_t most = (N + 63) / 64;  // at least 64 rows each
-  if (c > most) c = most;
-  return c < 1 ? 1 : c;
-}
-
-cudaError_t launch_colsum(const void* dS, int dtype, int B, int64_t N, int K, float* part, float* dbias,
-                          cudaStream_t s) {
-  const int64_t chunks = colsum_chunks(B, N, K);
-  const int64_t chunk = (N + chunks - 1) / chunks;
-  cudaError_t e = plain_launch();
-  if (e != cudaSuccess) return e;
-  const unsigned grid = static_cast<unsigned>((K + 127) / 128 * chunks * B);
-  if (dtype == kDtypeBF16) k_colsum<true><<<grid, 128, 0, s>>>(dS, N, K, chunk, chunks, part);
-  else k_colsum<false><<<grid, 128, 0, s>>>(dS, N, K, chunk, chunks, part);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  e = plain_launch();
-  if (e != cudaSuccess) return e;
-  const int64_t n = static_cast<int64_t>(B) * K;
-  k_colsum_join<<<grid_of(n), kT, 0, s>>>(part, chunks, n, K, dbias);
   return cudaGetLastError();
 }
 

@@ -57,8 +57,7 @@ struct Layout {
   size_t off_cop = 0, off_xop = 0, off_planes = 0, off_parts = 0, off_cols = 0, off_bal = 0, total = 0;
   int planes = 1;
   bool copy_ds = false;
-  int splits = 1;
-  int64_t split_len = 0;
+  GradPlan gp{};
 };
 
 int make_layout(Layout& l, int op, int B, int64_t N, int D, int K, int dtype) {
@@ -80,19 +79,9 @@ int make_layout(Layout& l, int op, int B, int64_t N, int D, int K, int dtype) {
     l.planes = dtype == KM_F32 ? 3 : 1;
     l.copy_ds = dtype == KM_F32 || K % 8 != 0;  // the tensor maps need rows of 16 bytes
     if (l.copy_ds) l.off_planes = take(static_cast<size_t>(l.planes) * B * N * ceil8(K) * 2);
-    // dC's tiles are few and its sums long: pieces of the points, enough to
-    // fill the SMs once, of at least 512 points
-    const int bn = grad_mm_tile(D);
-    const int64_t tiles = static_cast<int64_t>(B) * ((K + 127) / 128) * ((D + bn - 1) / bn);
-    int64_t sp = tiles < 148 ? 148 / tiles : 1;
-    if (sp > (N + 511) / 512) sp = (N + 511) / 512;
-    if (sp < 1) sp = 1;
-    l.split_len = ((N + sp - 1) / sp + 63) / 64 * 64;
-    if (l.split_len < 64) l.split_len = 64;
-    l.splits = static_cast<int>((N + l.split_len - 1) / l.split_len);
-    if (l.splits < 1) l.splits = 1;
-    if (l.splits > 1) l.off_parts = take(sizeof(float) * l.splits * static_cast<size_t>(B) * K * D);
-    l.off_cols = take(sizeof(float) * static_cast<size_t>(B) * colsum_chunks(B, N, K) * K);
+    l.gp = grad_plan(B, N, D, K);
+    if (l.gp.splits > 1) l.off_parts = take(sizeof(float) * l.gp.splits * static_cast<size_t>(B) * K * D);
+    l.off_cols = take(sizeof(float) * l.gp.splits * l.gp.parts * static_cast<size_t>(B) * K);
   } else if (op == KM_SOFT_BALANCE) {
     l.off_bal = take(sizeof(double) * static_cast<size_t>(B) * balance_blocks(B, N));
   }
@@ -232,50 +221,41 @@ int km_scores_grad(const void* dS, const uint8_t* xq, const uint8_t* xs, const u
   void* cop = c.ws + l.off_cop;
   void* xop = c.ws + l.off_xop;
   const void* ds = dS;
-  if ((dX || dC) && l.copy_ds) {
+  if (l.copy_ds) {
     void* planes = c.ws + l.off_planes;
     SOFT_CUDA(launch_split_planes(dS, dtype, static_cast<int64_t>(B) * N, K, ldk, planes, c.s));
     ds = planes;
   }
-  CUtensorMap amap, bmap;
-  GradMmArgs a{};
-  a.amap = &amap;
-  a.bmap = &bmap;
+  if (dX) SOFT_CUDA(launch_dequantize(cq, cs, KM_BF16, static_cast<int64_t>(B) * K, D, ldd, cop, c.s));
+  if (dC) SOFT_CUDA(launch_dequantize(xq, xs, KM_BF16, static_cast<int64_t>(B) * N, D, ldd, xop, c.s));
+  CUtensorMap ds_x, ds_c, cmap, xmap;
+  const int64_t depth = static_cast<int64_t>(l.planes) * B;
+  if ((r = encode_bf16(&ds_x, ds, K, ldk, N, depth, 256)) != KM_OK) return r;
+  if ((r = encode_bf16(&ds_c, ds, K, ldk, N, depth, 64)) != KM_OK) return r;
+  if ((r = encode_bf16(&cmap, cop, D, ldd, K, B, 64)) != KM_OK) return r;
+  if ((r = encode_bf16(&xmap, xop, D, ldd, N, B, 64)) != KM_OK) return r;
+  GradArgs a{};
+  a.ds_x = &ds_x;
+  a.ds_c = &ds_c;
+  a.cmap = &cmap;
+  a.xmap = &xmap;
   a.planes = l.planes;
   a.B = B;
+  a.N = N;
   a.D = D;
+  a.K = K;
   a.alpha = alpha;
+  a.dx_dtype = dx_dtype;
+  a.dX = dX;
+  float* parts = l.gp.splits > 1 ? reinterpret_cast<float*>(c.ws + l.off_parts) : dC;
+  a.dC = dC ? parts : nullptr;
+  a.db = dbias ? reinterpret_cast<float*>(c.ws + l.off_cols) : nullptr;
   a.status = c.status();
   a.limit_ns = api_wait_limit_ns();
-  if (dX) {
-    SOFT_CUDA(launch_dequantize(cq, cs, KM_BF16, static_cast<int64_t>(B) * K, D, ldd, cop, c.s));
-    if ((r = encode_bf16(&amap, ds, K, ldk, N, static_cast<int64_t>(l.planes) * B, 128)) != KM_OK) return r;
-    if ((r = encode_bf16(&bmap, cop, D, ldd, K, B, 64)) != KM_OK) return r;
-    a.transposed = false;
-    a.M = N;
-    a.L = K;
-    a.splits = 1;
-    a.split_len = (static_cast<int64_t>(K) + 63) / 64 * 64;
-    a.out_dtype = dx_dtype;
-    a.out = dX;
-    SOFT_CUDA(launch_grad_mm(a, c.s));
-  }
-  if (dC) {
-    SOFT_CUDA(launch_dequantize(xq, xs, KM_BF16, static_cast<int64_t>(B) * N, D, ldd, xop, c.s));
-    if ((r = encode_bf16(&amap, ds, K, ldk, N, static_cast<int64_t>(l.planes) * B, 64)) != KM_OK) return r;
-    if ((r = encode_bf16(&bmap, xop, D, ldd, N, B, 64)) != KM_OK) return r;
-    a.transposed = true;
-    a.M = K;
-    a.L = N;
-    a.splits = l.splits;
-    a.split_len = l.split_len;
-    a.out_dtype = KM_F32;
-    a.out = l.splits > 1 ? reinterpret_cast<float*>(c.ws + l.off_parts) : dC;
-    SOFT_CUDA(launch_grad_mm(a, c.s));
-    if (l.splits > 1)
-      SOFT_CUDA(launch_split_sum(static_cast<const float*>(a.out), l.splits, static_cast<int64_t>(B) * K * D, dC, c.s));
-  }
-  if (dbias) SOFT_CUDA(launch_colsum(dS, dtype, B, N, K, reinterpret_cast<float*>(c.ws + l.off_cols), dbias, c.s));
+  SOFT_CUDA(launch_grad(a, c.s));
+  const int64_t nc = dC && l.gp.splits > 1 ? static_cast<int64_t>(B) * K * D : 0;
+  const int64_t nb = dbias ? static_cast<int64_t>(B) * K : 0;
+  if (nc + nb) SOFT_CUDA(launch_grad_join(parts, l.gp.splits, nc, dC, a.db, l.gp.splits * l.gp.parts, nb, dbias, c.s));
   return KM_OK;
 }
 

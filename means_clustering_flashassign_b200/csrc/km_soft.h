@@ -56,39 +56,42 @@ struct ScoresArgs {
 cudaError_t launch_scores(const ScoresArgs& a, cudaStream_t s);
 
 // ------------------------------------------------------------ score gradients
-// One product of the gradient: out[m][n] = alpha * sum_l A(m, l) * Bm[l][n],
-// A being the score gradients dS (planes bf16 matrices whose sum is dS), Bm
-// the operand the scores were taken from, in bf16 (exact for 8-bit points).
-struct GradMmArgs {
-  bool transposed;           // false: A(m, l) = dS[m][l] (dX); true: A(m, l) = dS[l][m] (dC)
-  const CUtensorMap* amap;   // [planes * B][N][K] bf16; box 64 x 128 rows, or 64 x 64 rows transposed
-  const CUtensorMap* bmap;   // [B][L][D] bf16, box 64 x 64 rows
-  int planes;
+constexpr int kGradCtas = 148;  // one per SM
+
+// How launch_grad cuts a shape up (k_grad.cu): centroids per tile, tiles,
+// CTAs per group, tiles per CTA, groups, pieces of an instance's points (each
+// with its own dC) and partial column sums per piece.
+struct GradPlan {
+  int kt, nkt, group, passes, splits, parts;
+  int64_t groups;
+};
+GradPlan grad_plan(int B, int64_t N, int D, int K);
+
+struct GradArgs {
+  const CUtensorMap* ds_x;  // [planes * B][N][K] bf16, box 64 centroids x 256 points
+  const CUtensorMap* ds_c;  // the same, box 64 centroids x 64 points
+  const CUtensorMap* cmap;  // [B][K][D] bf16, box 64 coordinates x 64 centroids
+  const CUtensorMap* xmap;  // [B][N][D] bf16, box 64 coordinates x 64 points
+  int planes;               // bf16 matrices whose sum is dS
   int B;
-  int64_t M;                 // rows of the output per instance
-  int64_t L;                 // length of the sum
-  int D;                     // columns of the output
-  int splits;                // pieces of the sum, each with its own output plane [split][B][M][D]
-  int64_t split_len;         // rows of the sum per piece (a multiple of 64)
+  int64_t N;
+  int D, K;
   float alpha;
-  int out_dtype;
-  void* out;
+  int dx_dtype;
+  void* dX;   // or null
+  float* dC;  // [splits][B][K][D] or null
+  float* db;  // [splits * parts][B][K] or null
   unsigned int* status;
   uint64_t limit_ns;
 };
-cudaError_t launch_grad_mm(const GradMmArgs& a, cudaStream_t s);
-// Width of the output tile launch_grad_mm uses for D columns.
-int grad_mm_tile(int D);
-// out[i] = sum over splits of part[split][i], in split order.
-cudaError_t launch_split_sum(const float* part, int splits, int64_t n, float* out, cudaStream_t s);
+cudaError_t launch_grad(const GradArgs& a, cudaStream_t s);
+// dC and dbias as the sums of their pieces, in order (nc or nb 0: left out).
+cudaError_t launch_grad_join(const float* cpart, int csplits, int64_t nc, float* dC, const float* bpart, int bsplits,
+                             int64_t nb, float* dbias, cudaStream_t s);
 // dS (dtype) as 1 (bf16) or 3 (f32) bf16 planes [planes][rows][ld]; the planes sum to dS
 // exactly for values whose third piece does not underflow.
 cudaError_t launch_split_planes(const void* dS, int dtype, int64_t rows, int K, int64_t ld, void* planes,
                                 cudaStream_t s);
-// dbias[b][k] = sum_i dS[b][i][k] through part [B][chunks][K].
-int64_t colsum_chunks(int B, int64_t N, int K);
-cudaError_t launch_colsum(const void* dS, int dtype, int B, int64_t N, int K, float* part, float* dbias,
-                          cudaStream_t s);
 
 // ---------------------------------------------------------------- balance
 struct BalanceArgs {
