@@ -397,21 +397,37 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------ small kernels
 constexpr int kT = 256;
 
-// out[i] = sum over the pieces, in order, for dC (nc elements) and dbias (nb).
+// out[i] = sum over the pieces, for dC (nc elements) and dbias (nb): 32 outputs
+// per block, 8 threads for each, every thread's pieces in order and then the 8
+// in order (the pieces of a small problem are many and its outputs few).
+constexpr int kJoinX = 32, kJoinY = 8;
+template <typename Acc>
+__device__ __forceinline__ Acc join_pieces(const float* part, int pieces, int64_t stride, int64_t i, int ty) {
+  Acc v = 0;
+#pragma unroll 4
+  for (int s = ty; s < pieces; s += kJoinY) v += part[static_cast<int64_t>(s) * stride + i];
+  return v;
+}
 __global__ void __launch_bounds__(kT) k_grad_join(const float* __restrict__ cpart, int csplits, int64_t nc,
                                                   float* __restrict__ dC, const float* __restrict__ bpart, int bsplits,
                                                   int64_t nb, float* __restrict__ dbias) {
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kT + threadIdx.x; i < nc + nb;
-       i += static_cast<int64_t>(gridDim.x) * kT) {
-    if (i < nc) {
-      float v = 0.f;
-      for (int s = 0; s < csplits; ++s) v += cpart[static_cast<int64_t>(s) * nc + i];
-      dC[i] = v;
-    } else {
-      double v = 0.0;
-      for (int s = 0; s < bsplits; ++s) v += bpart[static_cast<int64_t>(s) * nb + i - nc];
-      dbias[i - nc] = static_cast<float>(v);
+  __shared__ double sum[kJoinY][kJoinX];
+  const int tx = threadIdx.x % kJoinX, ty = threadIdx.x / kJoinX;
+  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kJoinX; i0 < nc + nb;
+       i0 += static_cast<int64_t>(gridDim.x) * kJoinX) {
+    const int64_t i = i0 + tx;
+    double v = 0.0;
+    if (i < nc) v = join_pieces<float>(cpart, csplits, nc, i, ty);
+    else if (i < nc + nb) v = join_pieces<double>(bpart, bsplits, nb, i - nc, ty);
+    sum[ty][tx] = v;
+    __syncthreads();
+    if (ty == 0 && i < nc + nb) {
+#pragma unroll
+      for (int j = 1; j < kJoinY; ++j) v += sum[j][tx];
+      if (i < nc) dC[i] = static_cast<float>(v);
+      else dbias[i - nc] = static_cast<float>(v);
     }
+    __syncthreads();
   }
 }
 
@@ -541,7 +557,7 @@ cudaError_t launch_grad_join(const float* cpart, int csplits, int64_t nc, float*
                              int64_t nb, float* dbias, cudaStream_t s) {
   cudaError_t e = plain_launch();
   if (e != cudaSuccess) return e;
-  k_grad_join<<<grid_of(nc + nb), kT, 0, s>>>(cpart, csplits, nc, dC, bpart, bsplits, nb, dbias);
+  k_grad_join<<<grid_of((nc + nb) * kJoinY), kT, 0, s>>>(cpart, csplits, nc, dC, bpart, bsplits, nb, dbias);
   return cudaGetLastError();
 }
 

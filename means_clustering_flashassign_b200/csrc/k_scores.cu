@@ -10,14 +10,20 @@
 // the same byte (the scale data id of the instruction descriptor), and one
 // 32-bit TMEM word per row carries the scales of four blocks.
 //
-// Structure: persistent CTAs (one per SM), warp-specialised:
-//   warp 0        TMA producer: 128-coordinate blocks of 128 points and 128
-//                 centroids (16 KB each, 128-byte swizzle) through a ring;
+// Writing S bounds narrow points (D <= 256: at D = 128 a bf16 tile of S is as
+// large as both its operands).  k_scores_near keeps a run of centroid tiles in
+// shared memory for a whole range of points, so that the only other traffic is
+// X, once per run.  Wider points go through k_scores_wide, which streams both
+// operands in 128-coordinate blocks.
+//
+// Structure of both: persistent CTAs (one per SM), warp-specialised:
+//   warp 0        TMA producer (blocks of 128 rows x 128 coordinates, 16 KB,
+//                 128-byte swizzle);
 //   warp 1        MMA issuer (one thread);
-//   warps 4..7    scales: the tile's scale bytes from global memory into TMEM,
-//                 four blocks at a time, in the layout the MMA reads (row r in
-//                 lane r % 32, column r / 32, repeated in each lane quarter);
-//   warps 8..15   epilogue: two groups, one per accumulator; alpha, bias,
+//   warps 4..7    scales: the scale bytes from global memory into TMEM, four
+//                 blocks at a time, in the layout the MMA reads (row r in lane
+//                 r % 32, column r / 32, repeated in each lane quarter);
+//   warps 8..19   epilogue: three groups, one per accumulator; alpha, bias,
 //                 rounding, and whole 128-byte lines to S through shared memory.
 // Every wait is bounded in time (km_ptx.cuh).
 #include "km_internal.h"
@@ -28,16 +34,27 @@ namespace km {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kAccs = 3;                 // accumulators, each with its epilogue group
+constexpr int kEpiWarps = 4 * kAccs;
+constexpr int kThreads = 32 * (8 + kEpiWarps);
 constexpr int kBM = 128, kBN = 128;
-constexpr int kStages = 5;
 constexpr int kOpBytes = kBM * kQBlock;  // 16 KB: 128 rows of one block
+constexpr uint32_t kTmemCols = 512;      // the accumulators and the scales (powers of two only)
+constexpr uint32_t kSfBase = kAccs * kBN;
+constexpr int kEpiBytes = kStageBytes + kBN * 4;  // a warp's staging rows and its copy of the tile's bias
+// k_scores_wide: stages of one block of each operand, stages of scales
+constexpr int kStages = 5;
 constexpr int kStageOps = 2 * kOpBytes;
 constexpr int kSfStages = 8;
 constexpr int kSfCols = 8;               // 4 TMEM columns of scales per operand
-constexpr uint32_t kTmemCols = 512;      // 2 accumulators + the scale ring (powers of two only)
-constexpr uint32_t kSfBase = 2 * kBN;
-constexpr size_t kSmem = 1024 + kStages * kStageOps + 8 * kStageBytes + 64 * 8;
+// k_scores_near: operand tiles in all; point tiles and their scales are double
+// and four times buffered, the rest holds centroid tiles
+constexpr int kNearTiles = 10;
+constexpr int kNearSfA = 4;
+constexpr int kNearMaxRun = 8;           // centroid tiles held (and 4 TMEM columns of scales for each)
+constexpr size_t kSmem = 1024 + kNearTiles * kOpBytes + kEpiWarps * kEpiBytes + 64 * 8;
+static_assert(kNearTiles * kOpBytes == kStages * kStageOps, "one shared-memory layout for both kernels");
+static_assert(kSfBase + kSfStages * kSfCols <= kTmemCols && kSfBase + 4 * (kNearMaxRun + kNearSfA) <= kTmemCols, "TMEM");
 
 struct ScoresK {
   const uint8_t* xs;
@@ -47,7 +64,9 @@ struct ScoresK {
   int B, K, nb, D;
   int64_t N;
   int64_t mt, nt;  // tiles per instance
-  int64_t ntiles;
+  int64_t ntiles;  // k_scores_wide
+  int run;         // k_scores_near: centroid tiles held together
+  int64_t runs, units;  // runs per instance, (instance, run, point tile) triples
   void* S;
   bool vec;
   unsigned int* status;
@@ -101,52 +120,326 @@ __device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int64_t row, in
   return w;
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads, 1)
-    k_scores(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap cmap, const ScoresK p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* ops = base;
-  uint8_t* staging = ops + kStages * kStageOps;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + 8 * kStageBytes);
-  uint64_t* full = bars;                      // [kStages]
-  uint64_t* empty = bars + 8;                 // [kStages]
-  uint64_t* sf_full = bars + 16;              // [kSfStages]
-  uint64_t* sf_empty = bars + 24;             // [kSfStages]
-  uint64_t* a_full = bars + 32;               // [2]
-  uint64_t* a_empty = bars + 34;              // [2]
-  uint64_t* drain = bars + 36;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 37);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// The bias of the tile's columns for this warp, 4 per lane (0 where there is none).
+__device__ __forceinline__ float4 load_bias(const ScoresK& p, int b, int n0, int lane) {
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (p.bias) {
+    const float* s = p.bias + static_cast<int64_t>(b) * p.K;
+    const int c = n0 + lane * 4;
+    if (c < p.K) v.x = __ldg(s + c);
+    if (c + 1 < p.K) v.y = __ldg(s + c + 1);
+    if (c + 2 < p.K) v.z = __ldg(s + c + 2);
+    if (c + 3 < p.K) v.w = __ldg(s + c + 3);
+  }
+  return v;
+}
 
+// One accumulator to S: 32 points per warp, the tile's 128 columns in staged
+// lines of 128 bytes; the TMEM loads run one 32-column chunk ahead.  buf is
+// the warp's staging rows and, behind them, its bias.
+template <bool BF16>
+__device__ __forceinline__ void emit_tile(const ScoresK& p, int b, int64_t m, int n0, uint32_t tm, uint64_t* empty,
+                                          uint8_t* buf, float4 bias4, int lane) {
+  constexpr int ES = BF16 ? 2 : 4;
+  constexpr int kCols = 128 / ES;  // columns of a staged line
+  const int rows = static_cast<int>(m + 32 <= p.N ? 32 : (p.N > m ? p.N - m : 0));
+  const int64_t row_bytes = static_cast<int64_t>(p.K) * ES;
+  uint8_t* out = static_cast<uint8_t*>(p.S) + (static_cast<int64_t>(b) * p.N + m) * row_bytes +
+                 static_cast<int64_t>(n0) * ES;
+  const int ncol = p.K - n0 < kBN ? p.K - n0 : kBN;
+  float* bias = reinterpret_cast<float*>(buf + kStageBytes);
+  reinterpret_cast<float4*>(bias)[lane] = bias4;
+  __syncwarp();
+  uint32_t r[2][32];
+  tmem_load32(tm, r[0]);
+  tmem_wait32(r[0]);
+#pragma unroll
+  for (int c = 0; c < kBN / 32; ++c) {
+    if (c + 1 < kBN / 32) tmem_load32(tm + static_cast<uint32_t>((c + 1) * 32), r[(c + 1) & 1]);
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 bv = reinterpret_cast<const float4*>(bias + c * 32)[i];
+      v[4 * i] = fmaf(__uint_as_float(r[c & 1][4 * i]), p.alpha, bv.x);
+      v[4 * i + 1] = fmaf(__uint_as_float(r[c & 1][4 * i + 1]), p.alpha, bv.y);
+      v[4 * i + 2] = fmaf(__uint_as_float(r[c & 1][4 * i + 2]), p.alpha, bv.z);
+      v[4 * i + 3] = fmaf(__uint_as_float(r[c & 1][4 * i + 3]), p.alpha, bv.w);
+    }
+    const int c0 = BF16 ? (c & ~1) * 32 : c * 32;  // first column of the staged line
+    if constexpr (BF16) stage_bf16(buf, v, c & 1, lane);
+    else stage_f32(buf, v, lane);
+    if (!BF16 || (c & 1)) {
+      __syncwarp();
+      const int n = ncol - c0 < kCols ? ncol - c0 : kCols;
+      if (n > 0) store_staged<ES>(buf, out + c0 * ES, row_bytes, rows, n * ES, p.vec, lane);
+      __syncwarp();
+    }
+    if (c + 1 < kBN / 32) {
+      tmem_wait32(r[(c + 1) & 1]);
+      if (c + 2 == kBN / 32) {  // the last chunk is in registers
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty);
+      }
+    }
+  }
+}
+
+// Barriers of both kernels.  near: op stages are point tiles (2) and bars.b_*
+// guard the centroid run; wide: op stages are blocks of both operands.
+struct Bars {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t sf_full[kSfStages], sf_empty[kSfStages];
+  uint64_t a_full[kAccs], a_empty[kAccs];
+  uint64_t b_full, b_empty, sfb_full;
+  uint64_t drain;
+  uint32_t tmem;
+  int abort_flag;
+};
+static_assert(sizeof(Bars) <= 64 * 8, "barrier space");
+
+struct Setup {
+  uint8_t* ops;
+  uint8_t* epi;
+  Bars* bars;
+  uint32_t tmem;
+};
+__device__ __forceinline__ Setup scores_setup(uint8_t* smem_raw) {
+  Setup s;
+  s.ops = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  s.epi = s.ops + kNearTiles * kOpBytes;
+  s.bars = reinterpret_cast<Bars*>(s.epi + kEpiWarps * kEpiBytes);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&s.bars->full[i], 1);
+      mbar_init(&s.bars->empty[i], 1);
     }
     for (int i = 0; i < kSfStages; ++i) {
-      mbar_init(&sf_full[i], 4);
-      mbar_init(&sf_empty[i], 1);
+      mbar_init(&s.bars->sf_full[i], 4);
+      mbar_init(&s.bars->sf_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&a_full[i], 1);
-      mbar_init(&a_empty[i], 4);
+    for (int i = 0; i < kAccs; ++i) {
+      mbar_init(&s.bars->a_full[i], 1);
+      mbar_init(&s.bars->a_empty[i], 4);
     }
-    mbar_init(drain, 1);
-    *abort_flag = 0;
+    mbar_init(&s.bars->b_full, 1);
+    mbar_init(&s.bars->b_empty, 1);
+    mbar_init(&s.bars->sfb_full, 4);
+    mbar_init(&s.bars->drain, 1);
+    s.bars->abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
   }
-  if (warp == 1) {
-    tmem_alloc(tmem_holder, kTmemCols);
+  if (threadIdx.x >> 5 == 1) {
+    tmem_alloc(&s.bars->tmem, kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_holder;
-  const WaitGuard g{p.status, abort_flag, p.limit_ns};
+  s.tmem = s.bars->tmem;
+  return s;
+}
+__device__ __forceinline__ void scores_teardown(const Setup& s) {
+  __syncthreads();
+  if (threadIdx.x >> 5 == 1) {
+    tc_fence_after();
+    tmem_dealloc(s.tmem, kTmemCols);
+  }
+}
+// Waits that must see their end even after another wait ran out.
+__device__ __forceinline__ void settle(uint64_t* bar, uint32_t phase, const WaitGuard& g) {
+  volatile int never = 0;
+  WaitGuard g2 = g;
+  g2.abort_flag = &never;
+  mbar_wait(bar, phase, g2);
+}
+__device__ __forceinline__ void store_scales(uint32_t taddr, const uint8_t* s, int64_t row0, int64_t rows, int nb, int k0,
+                                             int lane) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = scale_word(s, row0 + 32 * j + lane, rows, nb, k0);
+  tmem_store4(taddr, w);
+}
+__device__ __forceinline__ void publish_scales(uint64_t* bar, int lane) {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+// The MMAs of one 128-coordinate block.
+__device__ __forceinline__ void block_mma(uint32_t d, uint32_t a, uint32_t b, int kb, int D, uint32_t sfa, uint32_t sfb) {
+  const uint32_t id = static_cast<uint32_t>(kb & 3);
+  const int left = D - kb * kQBlock;
+  const int steps = left >= kQBlock ? 4 : (left + 31) / 32;
+  for (int s = 0; s < steps; ++s)
+    umma_mx(d, sw128_kmajor_desc(a + s * 32), sw128_kmajor_desc(b + s * 32), mx_idesc(id), sfa, sfb,
+            (kb | s) != 0 ? 1u : 0u);
+}
+
+// Narrow points: units (instance, run of centroid tiles, point tile), point
+// tiles fastest; a CTA takes consecutive units and reloads the centroids only
+// where the run changes.
+struct UnitPos {
+  int b, r;
+  int64_t m;
+  __device__ __forceinline__ UnitPos(int64_t u, const ScoresK& p) {
+    const int64_t q = u / p.mt;
+    m = u - q * p.mt;
+    b = static_cast<int>(q / p.runs);
+    r = static_cast<int>(q - static_cast<int64_t>(b) * p.runs);
+  }
+  __device__ __forceinline__ void next(const ScoresK& p) {
+    if (++m == p.mt) {
+      m = 0;
+      if (++r == p.runs) { r = 0; ++b; }
+    }
+  }
+  // centroid tiles of this run
+  __device__ __forceinline__ int tiles(const ScoresK& p) const {
+    const int64_t n = p.nt - static_cast<int64_t>(r) * p.run;
+    return n < p.run ? static_cast<int>(n) : p.run;
+  }
+};
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_scores_near(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap cmap, const ScoresK p) {
+  extern __shared__ uint8_t smem_raw[];
+  const Setup su = scores_setup(smem_raw);
+  Bars& bars = *su.bars;
+  const WaitGuard g{p.status, &bars.abort_flag, p.limit_ns};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nb = p.nb;
+  uint8_t* cops = su.ops + 2 * nb * kOpBytes;  // the centroid run, behind two point tiles
+  const int64_t u0 = blockIdx.x * p.units / gridDim.x, u1 = (blockIdx.x + 1) * p.units / gridDim.x;
+  const uint32_t sfb = su.tmem + kSfBase, sfa = sfb + 4 * kNearMaxRun;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      prefetch_tensormap(&xmap);
+      prefetch_tensormap(&cmap);
+      int st = 0, issued[2] = {-1, -1}, b_issued = -1;
+      uint32_t ph = 0, bph = 0;
+      UnitPos q(u0, p);
+      for (int64_t u = u0; u < u1; ++u, q.next(p)) {
+        if (u == u0 || q.m == 0) {
+          if (!mbar_wait(&bars.b_empty, bph ^ 1u, g)) break;
+          const int n = q.tiles(p);
+          mbar_arrive_expect_tx(&bars.b_full, static_cast<uint32_t>(n * nb * kOpBytes));
+          for (int j = 0; j < n; ++j)
+            for (int kb = 0; kb < nb; ++kb)
+              tma_load_3d(cops + (j * nb + kb) * kOpBytes, &cmap, kb * kQBlock, (q.r * p.run + j) * kBN, q.b, &bars.b_full);
+          b_issued = static_cast<int>(bph);
+          bph ^= 1u;
+        }
+        if (!mbar_wait(&bars.empty[st], ph ^ 1u, g)) break;
+        mbar_arrive_expect_tx(&bars.full[st], static_cast<uint32_t>(nb * kOpBytes));
+        for (int kb = 0; kb < nb; ++kb)
+          tma_load_3d(su.ops + (st * nb + kb) * kOpBytes, &xmap, kb * kQBlock, static_cast<int>(q.m * kBM), q.b,
+                      &bars.full[st]);
+        issued[st] = static_cast<int>(ph);
+        st ^= 1;
+        if (st == 0) ph ^= 1u;
+      }
+      // copies still in flight land before the CTA can exit (at once, unless a
+      // wait ran out)
+      for (int i = 0; i < 2; ++i)
+        if (issued[i] >= 0) settle(&bars.full[i], static_cast<uint32_t>(issued[i]), g);
+      if (b_issued >= 0) settle(&bars.b_full, static_cast<uint32_t>(b_issued), g);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int st = 0, ss = 0, ab = 0;
+      uint32_t ph = 0, sph = 0, aph = 0, bph = 0;
+      bool ok = true;
+      UnitPos q(u0, p);
+      for (int64_t u = u0; ok && u < u1; ++u) {
+        if (u == u0 || q.m == 0) {
+          if (!mbar_wait(&bars.b_full, bph, g) || !mbar_wait(&bars.sfb_full, bph, g)) break;
+          bph ^= 1u;
+        }
+        if (!mbar_wait(&bars.sf_full[ss], sph, g) || !mbar_wait(&bars.full[st], ph, g)) break;
+        const int n = q.tiles(p);
+        const uint32_t a = smem_addr(su.ops + st * nb * kOpBytes), c = smem_addr(cops);
+        for (int j = 0; j < n; ++j) {
+          if (!mbar_wait(&bars.a_empty[ab], aph ^ 1u, g)) { ok = false; break; }
+          tc_fence_after();
+          for (int kb = 0; kb < nb; ++kb)
+            block_mma(su.tmem + static_cast<uint32_t>(ab * kBN), a + kb * kOpBytes, c + (j * nb + kb) * kOpBytes, kb, p.D,
+                      sfa + static_cast<uint32_t>(4 * ss), sfb + static_cast<uint32_t>(4 * j));
+          umma_commit(&bars.a_full[ab]);
+          if (++ab == kAccs) { ab = 0; aph ^= 1u; }
+        }
+        if (!ok) break;
+        umma_commit(&bars.empty[st]);
+        umma_commit(&bars.sf_empty[ss]);
+        st ^= 1;
+        if (st == 0) ph ^= 1u;
+        if (++ss == kNearSfA) { ss = 0; sph ^= 1u; }
+        q.next(p);
+        if (q.m == 0) umma_commit(&bars.b_empty);
+      }
+      umma_commit(&bars.drain);  // every MMA is done before TMEM can be released
+      settle(&bars.drain, 0u, g);
+    }
+  } else if (warp >= 4 && warp < 8) {
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    int ss = 0;
+    uint32_t sph = 0, bph = 0;
+    UnitPos q(u0, p);
+    for (int64_t u = u0; u < u1; ++u, q.next(p)) {
+      if (u == u0 || q.m == 0) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars.b_empty, bph ^ 1u, g))) break;
+        bph ^= 1u;
+        tc_fence_after();
+        const int n = q.tiles(p);
+        for (int j = 0; j < n; ++j)
+          store_scales(sfb + lane_off + static_cast<uint32_t>(4 * j), p.cs + static_cast<int64_t>(q.b) * p.K * nb,
+                       static_cast<int64_t>(q.r * p.run + j) * kBN, p.K, nb, 0, lane);
+        publish_scales(&bars.sfb_full, lane);
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars.sf_empty[ss], sph ^ 1u, g))) break;
+      tc_fence_after();
+      store_scales(sfa + lane_off + static_cast<uint32_t>(4 * ss), p.xs + static_cast<int64_t>(q.b) * p.N * nb, q.m * kBM,
+                   p.N, nb, 0, lane);
+      publish_scales(&bars.sf_full[ss], lane);
+      if (++ss == kNearSfA) { ss = 0; sph ^= 1u; }
+    }
+  } else if (warp >= 8) {
+    const int q4 = warp & 3, grp = (warp - 8) >> 2;
+    const uint32_t tm = su.tmem + (static_cast<uint32_t>(q4 * 32) << 16) + static_cast<uint32_t>(grp * kBN);
+    uint8_t* buf = su.epi + (warp - 8) * kEpiBytes;
+    uint32_t aph = 0;
+    int ab = 0;
+    bool ok = true;
+    UnitPos q(u0, p);
+    for (int64_t u = u0; ok && u < u1; ++u, q.next(p)) {
+      const int n = q.tiles(p);
+      for (int j = 0; j < n; ++j) {
+        const bool mine = ab == grp;
+        if (++ab == kAccs) ab = 0;
+        if (!mine) continue;
+        const int n0 = (q.r * p.run + j) * kBN;
+        const float4 bias4 = load_bias(p, q.b, n0, lane);
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars.a_full[grp], aph, g))) { ok = false; break; }
+        aph ^= 1u;
+        tc_fence_after();
+        emit_tile<BF16>(p, q.b, q.m * kBM + q4 * 32, n0, tm, &bars.a_empty[grp], buf, bias4, lane);
+      }
+    }
+  }
+  scores_teardown(su);
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_scores_wide(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap cmap, const ScoresK p) {
+  extern __shared__ uint8_t smem_raw[];
+  const Setup su = scores_setup(smem_raw);
+  Bars& bars = *su.bars;
+  const WaitGuard g{p.status, &bars.abort_flag, p.limit_ns};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nb = p.nb;
 
   if (warp == 0) {
@@ -162,22 +455,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int64_t t = blockIdx.x; ok && t < p.ntiles; t += gridDim.x) {
         const TilePos tp = tile_pos(t, p);
         for (int kb = 0; kb < nb; ++kb) {
-          if (!mbar_wait(&empty[st], ph ^ 1u, g)) { ok = false; break; }
-          uint8_t* dst = ops + st * kStageOps;
-          mbar_arrive_expect_tx(&full[st], kStageOps);
-          tma_load_3d(dst, &xmap, kb * kQBlock, static_cast<int>(tp.m0), tp.b, &full[st]);
-          tma_load_3d(dst + kOpBytes, &cmap, kb * kQBlock, tp.n0, tp.b, &full[st]);
+          if (!mbar_wait(&bars.empty[st], ph ^ 1u, g)) { ok = false; break; }
+          uint8_t* dst = su.ops + st * kStageOps;
+          mbar_arrive_expect_tx(&bars.full[st], kStageOps);
+          tma_load_3d(dst, &xmap, kb * kQBlock, static_cast<int>(tp.m0), tp.b, &bars.full[st]);
+          tma_load_3d(dst + kOpBytes, &cmap, kb * kQBlock, tp.n0, tp.b, &bars.full[st]);
           issued[st] = static_cast<int>(ph);
           if (++st == kStages) { st = 0; ph ^= 1u; }
         }
       }
-      // copies still in flight land before the CTA can exit (at once, unless a
-      // wait ran out)
-      volatile int never = 0;
-      WaitGuard g2 = g;
-      g2.abort_flag = &never;
       for (int i = 0; i < kStages; ++i)
-        if (issued[i] >= 0) mbar_wait(&full[i], static_cast<uint32_t>(issued[i]), g2);
+        if (issued[i] >= 0) settle(&bars.full[i], static_cast<uint32_t>(issued[i]), g);
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -185,38 +473,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t ph = 0, sph = 0, aph = 0;
       bool ok = true;
       for (int64_t t = blockIdx.x; ok && t < p.ntiles; t += gridDim.x) {
-        if (!mbar_wait(&a_empty[ab], aph ^ 1u, g)) break;
-        const uint32_t d = tmem + static_cast<uint32_t>(ab * kBN);
+        if (!mbar_wait(&bars.a_empty[ab], aph ^ 1u, g)) break;
         for (int kb = 0; kb < nb; ++kb) {
-          const uint32_t id = static_cast<uint32_t>(kb & 3);
-          if (id == 0 && !mbar_wait(&sf_full[ss], sph, g)) { ok = false; break; }
-          if (!mbar_wait(&full[st], ph, g)) { ok = false; break; }
+          if ((kb & 3) == 0 && !mbar_wait(&bars.sf_full[ss], sph, g)) { ok = false; break; }
+          if (!mbar_wait(&bars.full[st], ph, g)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t a = smem_addr(ops + st * kStageOps);
-          const uint32_t sf = tmem + kSfBase + static_cast<uint32_t>(ss * kSfCols);
-          const int left = p.D - kb * kQBlock;
-          const int steps = left >= kQBlock ? 4 : (left + 31) / 32;
-          for (int s = 0; s < steps; ++s)
-            umma_mx(d, sw128_kmajor_desc(a + s * 32), sw128_kmajor_desc(a + kOpBytes + s * 32), mx_idesc(id), sf, sf + 4,
-                    (kb | s) != 0 ? 1u : 0u);
-          umma_commit(&empty[st]);
+          const uint32_t a = smem_addr(su.ops + st * kStageOps);
+          const uint32_t sf = su.tmem + kSfBase + static_cast<uint32_t>(ss * kSfCols);
+          block_mma(su.tmem + static_cast<uint32_t>(ab * kBN), a, a + kOpBytes, kb, p.D, sf, sf + 4);
+          umma_commit(&bars.empty[st]);
           if (++st == kStages) { st = 0; ph ^= 1u; }
-          if (id == 3 || kb == nb - 1) {
-            umma_commit(&sf_empty[ss]);
+          if ((kb & 3) == 3 || kb == nb - 1) {
+            umma_commit(&bars.sf_empty[ss]);
             if (++ss == kSfStages) { ss = 0; sph ^= 1u; }
           }
         }
         if (!ok) break;
-        umma_commit(&a_full[ab]);
-        ab ^= 1;
-        if (ab == 0) aph ^= 1u;
+        umma_commit(&bars.a_full[ab]);
+        if (++ab == kAccs) { ab = 0; aph ^= 1u; }
       }
-      // every MMA this thread issued is done before TMEM can be released
-      umma_commit(drain);
-      volatile int never = 0;
-      WaitGuard g2 = g;
-      g2.abort_flag = &never;
-      mbar_wait(drain, 0u, g2);
+      umma_commit(&bars.drain);  // every MMA is done before TMEM can be released
+      settle(&bars.drain, 0u, g);
     }
   } else if (warp >= 4 && warp < 8) {
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -225,86 +502,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int64_t t = blockIdx.x; ok && t < p.ntiles; t += gridDim.x) {
       const TilePos tp = tile_pos(t, p);
-      const uint8_t* xs = p.xs + static_cast<int64_t>(tp.b) * p.N * nb;
-      const uint8_t* cs = p.cs + static_cast<int64_t>(tp.b) * p.K * nb;
       for (int k0 = 0; k0 < nb; k0 += 4) {
-        uint32_t wx[4], wc[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          wx[j] = scale_word(xs, tp.m0 + 32 * j + lane, p.N, nb, k0);
-          wc[j] = scale_word(cs, tp.n0 + 32 * j + lane, p.K, nb, k0);
-        }
-        if (!__all_sync(0xffffffffu, mbar_wait(&sf_empty[ss], sph ^ 1u, g))) { ok = false; break; }
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars.sf_empty[ss], sph ^ 1u, g))) { ok = false; break; }
         tc_fence_after();
-        const uint32_t a = tmem + lane_off + kSfBase + static_cast<uint32_t>(ss * kSfCols);
-        tmem_store4(a, wx);
-        tmem_store4(a + 4, wc);
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sf_full[ss]);
+        const uint32_t a = su.tmem + lane_off + kSfBase + static_cast<uint32_t>(ss * kSfCols);
+        store_scales(a, p.xs + static_cast<int64_t>(tp.b) * p.N * nb, tp.m0, p.N, nb, k0, lane);
+        store_scales(a + 4, p.cs + static_cast<int64_t>(tp.b) * p.K * nb, tp.n0, p.K, nb, k0, lane);
+        publish_scales(&bars.sf_full[ss], lane);
         if (++ss == kSfStages) { ss = 0; sph ^= 1u; }
       }
     }
   } else if (warp >= 8) {
-    const int q = warp & 3, grp = (warp - 8) >> 2;
-    const uint32_t col0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(grp * kBN);
-    uint8_t* stage = staging + (warp - 8) * kStageBytes;
-    constexpr int ES = BF16 ? 2 : 4;
-    constexpr int kCols = 128 / ES;  // columns of a staged line
-    const int64_t row_bytes = static_cast<int64_t>(p.K) * ES;
+    const int q4 = warp & 3, grp = (warp - 8) >> 2;
+    const uint32_t tm = su.tmem + (static_cast<uint32_t>(q4 * 32) << 16) + static_cast<uint32_t>(grp * kBN);
+    uint8_t* buf = su.epi + (warp - 8) * kEpiBytes;
     uint32_t aph = 0;
-    int64_t seq = 0;
-    for (int64_t t = blockIdx.x; t < p.ntiles; t += gridDim.x, ++seq) {
-      if ((seq & 1) != grp) continue;
+    int ab = 0;
+    for (int64_t t = blockIdx.x; t < p.ntiles; t += gridDim.x) {
+      const bool mine = ab == grp;
+      if (++ab == kAccs) ab = 0;
+      if (!mine) continue;
       const TilePos tp = tile_pos(t, p);
-      const int64_t m = tp.m0 + q * 32;
-      const int rows = static_cast<int>(m + 32 <= p.N ? 32 : (p.N > m ? p.N - m : 0));
-      const float* bias = p.bias ? p.bias + static_cast<int64_t>(tp.b) * p.K + tp.n0 : nullptr;
-      uint8_t* out = static_cast<uint8_t*>(p.S) + (static_cast<int64_t>(tp.b) * p.N + m) * row_bytes +
-                     static_cast<int64_t>(tp.n0) * ES;
-      const int ncol = p.K - tp.n0 < kBN ? p.K - tp.n0 : kBN;
-      if (!__all_sync(0xffffffffu, mbar_wait(&a_full[grp], aph, g))) break;
+      const float4 bias4 = load_bias(p, tp.b, tp.n0, lane);
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars.a_full[grp], aph, g))) break;
       aph ^= 1u;
       tc_fence_after();
-#pragma unroll 1
-      for (int c = 0; c < kBN / 32; ++c) {
-        uint32_t r[32];
-        tmem_load32(col0 + static_cast<uint32_t>(c * 32), r);
-        tmem_wait32(r);
-        if (c == kBN / 32 - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&a_empty[grp]);
-        }
-        float v[32];
-        if (bias) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float bv = c * 32 + i < ncol ? __ldg(bias + c * 32 + i) : 0.f;
-            v[i] = fmaf(__uint_as_float(r[i]), p.alpha, bv);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * p.alpha;
-        }
-        const int c0 = BF16 ? (c & ~1) * 32 : c * 32;  // first column of the staged line
-        if constexpr (BF16) stage_bf16(stage, v, c & 1, lane);
-        else stage_f32(stage, v, lane);
-        if (!BF16 || (c & 1)) {
-          __syncwarp();
-          const int n = ncol - c0 < kCols ? ncol - c0 : kCols;
-          if (n > 0) store_staged<ES>(stage, out + c0 * ES, row_bytes, rows, n * ES, p.vec, lane);
-          __syncwarp();
-        }
-      }
+      emit_tile<BF16>(p, tp.b, tp.m0 + q4 * 32, tp.n0, tm, &bars.a_empty[grp], buf, bias4, lane);
     }
   }
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
-  }
+  scores_teardown(su);
 }
 
 }  // namespace
@@ -332,13 +558,28 @@ cudaError_t launch_scores(const ScoresArgs& a, cudaStream_t s) {
   int dev = 0, nsm = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
-  auto kern = a.dtype == kDtypeBF16 ? k_scores<true> : k_scores<false>;
+  // Narrow points keep centroid runs in shared memory: two point tiles of nb
+  // blocks each leave room for (10 - 2 nb) / nb centroid tiles; shorter runs
+  // where the units would not occupy every SM.
+  const bool near = k.nb <= 2;
+  int64_t grid = k.ntiles;
+  if (near) {
+    int64_t run = (kNearTiles - 2 * k.nb) / k.nb;
+    if (run > k.nt) run = k.nt;
+    while (run > 1 && a.B * ((k.nt + run - 1) / run) * k.mt < nsm) --run;
+    k.run = static_cast<int>(run);
+    k.runs = (k.nt + run - 1) / run;
+    k.units = a.B * k.runs * k.mt;
+    grid = k.units;
+  }
+  const bool bf16 = a.dtype == kDtypeBF16;
+  auto kern = near ? (bf16 ? k_scores_near<true> : k_scores_near<false>) : (bf16 ? k_scores_wide<true> : k_scores_wide<false>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
   if (e != cudaSuccess) return e;
   chain_break();
   if (fault_hit(kFaultLaunch)) return cudaErrorLaunchFailure;
   count_launch();
-  kern<<<static_cast<unsigned>(k.ntiles < nsm ? k.ntiles : nsm), kThreads, kSmem, s>>>(*a.xmap, *a.cmap, k);
+  kern<<<static_cast<unsigned>(grid < nsm ? grid : nsm), kThreads, kSmem, s>>>(*a.xmap, *a.cmap, k);
   return cudaGetLastError();
 }
 
