@@ -11,12 +11,20 @@
 // numbers.  Softmax sums, r_i and the loss's terms are float32, the loss's sum
 // over the rows float64 in a fixed order; counts are integers (any order of
 // the adds gives the same ones).
+//
+// Both row passes are bound by HBM once a row costs few enough instructions
+// and shared-memory-pipe cycles.  A group of 1 to 256 threads holds a row in
+// registers (32 elements a thread at most) and, across all its rows, the shares
+// f of its own columns: fetching those again for every row took more load
+// cycles than the row itself (79 % of the load pipe's, at 2.7 TB/s).  Rows
+// wider than 8192 go through the block in pieces, with running maxima.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
 #include <type_traits>
 
 #include "km_internal.h"
+#include "km_ptx.cuh"
 #include "km_soft.h"
 
 namespace km {
@@ -26,29 +34,319 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kHistMax = 8192;  // clusters a block counts in shared memory
+constexpr int kRegCols = 32;    // columns of a row per thread, at most
+constexpr float kLog2e = 1.4426950408889634f;
 
 template <bool BF16>
 using elem_t = typename std::conditional<BF16, __nv_bfloat16, float>::type;
 
+// exp(x) for x <= 0 (or NaN): 2^(x log2 e), whose rounded argument is off by
+// |x| 2^-24 -- no more than x, a difference of two float32 scores, is itself.
+// The difference comes first: a score near the type's lowest value times log2 e
+// would overflow.
+__device__ __forceinline__ float exp_of(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x * kLog2e));
+  return y;
+}
+
+struct BalK {
+  const int32_t* idx;
+  const uint8_t* valid;
+  int64_t N;
+  int K, T, nblk;
+  float* loss;
+  int32_t* counts;
+  int32_t* rows;
+  float* lse;
+  float* dot;
+  double* part;        // [B][nblk]
+  unsigned int* done;  // [B] blocks that have added their part
+  const float* grad;
+};
+
+// ------------------------------------------------------------------ counts
+__global__ void __launch_bounds__(kThreads) k_bal_zero(BalK p, int64_t nc, int B) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  for (int64_t j = i; j < nc; j += static_cast<int64_t>(gridDim.x) * kThreads) p.counts[j] = 0;
+  if (i < B) p.rows[i] = 0, p.done[i] = 0;
+}
+
+// counts[b][k] += picks of valid points; rows[b] += valid points.  Blocks of an
+// instance take its points round robin; one block alone (SOLO) writes its
+// histogram without adding, so that nothing has to be zeroed before.
+template <bool SOLO>
+__global__ void __launch_bounds__(kThreads) k_bal_count(BalK p, int nblk) {
+  extern __shared__ int32_t hist[];
+  __shared__ int32_t valid_rows;
+  const int b = blockIdx.x / nblk, blk = blockIdx.x - b * nblk;
+  const bool local = SOLO || p.K <= kHistMax;
+  if (threadIdx.x == 0) valid_rows = 0;
+  if (local)
+    for (int k = threadIdx.x; k < p.K; k += kThreads) hist[k] = 0;
+  __syncthreads();
+  pdl_wait();
+  const int32_t* idx = p.idx + b * p.N * p.T;
+  const uint8_t* valid = p.valid ? p.valid + b * p.N : nullptr;
+  int32_t* counts = p.counts + static_cast<int64_t>(b) * p.K;
+  int n = 0;
+  for (int64_t i = static_cast<int64_t>(blk) * kThreads + threadIdx.x; i < p.N;
+       i += static_cast<int64_t>(nblk) * kThreads) {
+    if (valid && !valid[i]) continue;
+    ++n;
+    for (int t = 0; t < p.T; ++t) {
+      const int k = idx[i * p.T + t];
+      if (k >= 0 && k < p.K) atomicAdd(local ? &hist[k] : &counts[k], 1);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  if ((threadIdx.x & 31) == 0 && n) atomicAdd(&valid_rows, n);
+  __syncthreads();
+  if (SOLO) {
+    for (int k = threadIdx.x; k < p.K; k += kThreads) counts[k] = hist[k];
+    if (threadIdx.x == 0) p.rows[b] = valid_rows, p.done[b] = 0;
+  } else {
+    if (local)
+      for (int k = threadIdx.x; k < p.K; k += kThreads)
+        if (hist[k]) atomicAdd(&counts[k], hist[k]);
+    if (threadIdx.x == 0 && valid_rows) atomicAdd(&p.rows[b], valid_rows);
+  }
+}
+
+// ----------------------------------------------------------- rows in registers
+// A thread's share of a row: NC chunks of V columns, chunk j at column
+// (j * LPR + l) * V (LPR threads per row, l this one's place among them).  V is
+// 16 bytes' worth where every row starts on a 16-byte boundary, else 1.
+template <bool BF16, bool VEC, int NC>
+struct Raw {
+  using Word = typename std::conditional<VEC, uint4, typename std::conditional<BF16, uint16_t, uint32_t>::type>::type;
+  Word w[NC];
+};
+
+template <bool BF16, bool VEC, int LPR, int NC>
+__device__ __forceinline__ void load_raw(Raw<BF16, VEC, NC>& r, const elem_t<BF16>* row, int K, int l, bool on) {
+  constexpr int V = VEC ? (BF16 ? 8 : 4) : 1;
+  using Word = typename Raw<BF16, VEC, NC>::Word;
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    const int c = (j * LPR + l) * V;
+    if (on && c < K) r.w[j] = __ldcs(reinterpret_cast<const Word*>(row + c));
+  }
+}
+
+// The columns' values (-inf behind the row's end).
+template <bool BF16, bool VEC, int LPR, int NC, int E>
+__device__ __forceinline__ void unpack_raw(const Raw<BF16, VEC, NC>& r, int K, int l, float (&x)[E]) {
+  constexpr int V = VEC ? (BF16 ? 8 : 4) : 1;
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    const bool in = (j * LPR + l) * V < K;
+    if constexpr (VEC) {
+      const uint32_t w[4] = {r.w[j].x, r.w[j].y, r.w[j].z, r.w[j].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (BF16) {
+          x[j * V + 2 * i] = in ? __uint_as_float(w[i] << 16) : -CUDART_INF_F;
+          x[j * V + 2 * i + 1] = in ? __uint_as_float(w[i] & 0xffff0000u) : -CUDART_INF_F;
+        } else {
+          x[j * V + i] = in ? __uint_as_float(w[i]) : -CUDART_INF_F;
+        }
+      }
+    } else if constexpr (BF16) {
+      x[j] = in ? __uint_as_float(static_cast<uint32_t>(r.w[j]) << 16) : -CUDART_INF_F;
+    } else {
+      x[j] = in ? __uint_as_float(r.w[j]) : -CUDART_INF_F;
+    }
+  }
+}
+
+// The shares of this thread's columns.
+template <int V, int LPR, int NC, int E>
+__device__ __forceinline__ void load_shares(const int32_t* counts, int K, int l, float inv, float (&f)[E]) {
+#pragma unroll
+  for (int j = 0; j < NC; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = (j * LPR + l) * V + i;
+      f[j * V + i] = c < K ? static_cast<float>(counts[c]) * inv : 0.f;
+    }
+}
+
+__device__ __forceinline__ float share_unit(int64_t M, int T) {
+  return M > 0 ? 1.f / (static_cast<float>(M) * static_cast<float>(T)) : 0.f;
+}
+
+// Maximum (or sum) over the LPR threads of a row; above a warp through shared
+// memory, where every thread of the block takes part.
+template <int LPR, bool MAX>
+__device__ __forceinline__ float row_reduce(float v, float* sm) {
+#pragma unroll
+  for (int o = (LPR < 32 ? LPR : 32) / 2; o > 0; o >>= 1) {
+    const float u = __shfl_xor_sync(0xffffffffu, v, o);
+    v = MAX ? fmaxf(v, u) : v + u;
+  }
+  if constexpr (LPR > 32) {
+    constexpr int W = LPR / 32;
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) sm[warp] = v;
+    __syncthreads();
+    v = sm[warp / W * W];
+#pragma unroll
+    for (int i = 1; i < W; ++i) v = MAX ? fmaxf(v, sm[warp / W * W + i]) : v + sm[warp / W * W + i];
+  }
+  return v;
+}
+
+// Adds the blocks' parts in order once the last of an instance has come: its
+// loss.  (The order of the blocks' arrival decides only who adds.)
+__device__ __forceinline__ void finish_loss(const BalK& p, int b, int blk, double sum) {
+  __shared__ double wsum[kWarps];
+  __shared__ bool last;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if ((threadIdx.x & 31) == 0) wsum[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double v = 0.0;
+    for (int w = 0; w < kWarps; ++w) v += wsum[w];
+    p.part[static_cast<int64_t>(b) * p.nblk + blk] = v;
+    __threadfence();
+    last = atomicAdd(&p.done[b], 1u) == static_cast<unsigned>(p.nblk - 1);
+    __threadfence();
+  }
+  __syncthreads();
+  if (last && threadIdx.x < 32) {
+    double v = 0.0;
+    for (int i = threadIdx.x; i < p.nblk; i += 32) v += __ldcg(&p.part[static_cast<int64_t>(b) * p.nblk + i]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (threadIdx.x == 0) p.loss[b] = p.rows[b] > 0 ? static_cast<float>(v * p.K / p.rows[b]) : 0.f;
+  }
+}
+
+// A row's two numbers from its maximum and sums: a row with nothing in it (all
+// -inf) has no probabilities, so r = 0.
+struct RowNumbers {
+  float lse, r;
+};
+__device__ __forceinline__ RowNumbers row_numbers(float m, float s, float t) {
+  if (s == 0.f) return {-CUDART_INF_F, 0.f};
+  return {(m == -CUDART_INF_F ? 0.f : m) + logf(s), t / s};
+}
+
+template <bool BF16, bool VEC, int LPR, int NC>
+__global__ void __launch_bounds__(kThreads) k_bal_rows(const elem_t<BF16>* __restrict__ S, const BalK p) {
+  constexpr int V = VEC ? (BF16 ? 8 : 4) : 1, E = NC * V, RPB = kThreads / LPR;
+  __shared__ float sm[3][kWarps];
+  const int b = blockIdx.x / p.nblk, blk = blockIdx.x - b * p.nblk;
+  const int l = threadIdx.x % LPR;
+  pdl_wait();
+  float f[E];
+  load_shares<V, LPR, NC, E>(p.counts + static_cast<int64_t>(b) * p.K, p.K, l, share_unit(p.rows[b], p.T), f);
+  double sum = 0.0;
+  const int64_t step = static_cast<int64_t>(p.nblk) * RPB;
+  int64_t i = static_cast<int64_t>(blk) * RPB + threadIdx.x / LPR;
+  auto usable = [&](int64_t r) { return r < p.N && (!p.valid || p.valid[b * p.N + r]); };
+  bool on = usable(i);
+  Raw<BF16, VEC, NC> next{};
+  load_raw<BF16, VEC, LPR, NC>(next, S + (b * p.N + i) * p.K, p.K, l, on);
+  // every thread of the block runs the same rounds (the reductions may span it)
+  for (int64_t base = static_cast<int64_t>(blk) * RPB; base < p.N; base += step, i += step) {
+    float x[E];
+    unpack_raw<BF16, VEC, LPR, NC, E>(next, p.K, l, x);
+    const bool now = on;
+    on = usable(i + step);
+    load_raw<BF16, VEC, LPR, NC>(next, S + (b * p.N + i + step) * p.K, p.K, l, on);
+    float m = x[0];
+#pragma unroll
+    for (int j = 1; j < E; ++j) m = fmaxf(m, x[j]);
+    m = row_reduce<LPR, true>(m, sm[0]);
+    const float sh = m == -CUDART_INF_F ? 0.f : m;
+    float s = 0.f, t = 0.f;
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const float e = exp_of(x[j] - sh);
+      s += e;
+      t = fmaf(e, f[j], t);
+    }
+    s = row_reduce<LPR, false>(s, sm[1]);
+    t = row_reduce<LPR, false>(t, sm[2]);
+    if (l == 0 && i < p.N) {
+      const RowNumbers n = now ? row_numbers(m, s, t) : RowNumbers{0.f, 0.f};
+      p.lse[b * p.N + i] = n.lse;
+      p.dot[b * p.N + i] = n.r;
+      sum += n.r;
+    }
+  }
+  finish_loss(p, b, blk, sum);
+}
+
+template <bool BF16, bool VEC, int LPR, int NC>
+__global__ void __launch_bounds__(kThreads) k_bal_grad(const elem_t<BF16>* __restrict__ S,
+                                                       elem_t<BF16>* __restrict__ dS, const BalK p) {
+  constexpr int V = VEC ? (BF16 ? 8 : 4) : 1, E = NC * V, RPB = kThreads / LPR;
+  const int b = blockIdx.x / p.nblk, blk = blockIdx.x - b * p.nblk;
+  const int l = threadIdx.x % LPR;
+  const int64_t M = p.rows[b];
+  const float coef = M > 0 ? (p.grad ? p.grad[b] : 1.f) * static_cast<float>(p.K) / static_cast<float>(M) : 0.f;
+  float f[E];
+  load_shares<V, LPR, NC, E>(p.counts + static_cast<int64_t>(b) * p.K, p.K, l, share_unit(M, p.T), f);
+  const int64_t step = static_cast<int64_t>(p.nblk) * RPB;
+  for (int64_t i = static_cast<int64_t>(blk) * RPB + threadIdx.x / LPR; i < p.N; i += step) {
+    const int64_t o = b * p.N + i;
+    const float ls = p.lse[o], r = p.dot[o];
+    const bool on = (!p.valid || p.valid[o]) && ls != -CUDART_INF_F;
+    Raw<BF16, VEC, NC> raw{};
+    load_raw<BF16, VEC, LPR, NC>(raw, S + o * p.K, p.K, l, on);
+    float x[E];
+    unpack_raw<BF16, VEC, LPR, NC, E>(raw, p.K, l, x);
+    #pragma unroll
+    for (int j = 0; j < E; ++j) x[j] = on ? coef * exp_of(x[j] - ls) * (f[j] - r) : 0.f;
+    elem_t<BF16>* out = dS + o * p.K;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int c = (j * LPR + l) * V;
+      if (c >= p.K) continue;
+      if constexpr (VEC && BF16) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(x[j * V + 2 * k], x[j * V + 2 * k + 1]);
+          w[k] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        __stcs(reinterpret_cast<uint4*>(out + c), make_uint4(w[0], w[1], w[2], w[3]));
+      } else if constexpr (VEC) {
+        __stcs(reinterpret_cast<float4*>(out + c), make_float4(x[j * V], x[j * V + 1], x[j * V + 2], x[j * V + 3]));
+      } else if constexpr (BF16) {
+        out[c] = __float2bfloat16_rn(x[j]);
+      } else {
+        out[c] = x[j];
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ wide rows
 // The row's elements in order, 16 aligned bytes at a time where the row allows
 // it: f(values, first column, how many).  A row of an odd width starts between
 // two 16-byte boundaries; its first and last few elements go one by one.
 template <bool BF16, typename F>
-__device__ __forceinline__ void for_row(const elem_t<BF16>* row, int K, int lane, F&& f) {
+__device__ __forceinline__ void for_row(const elem_t<BF16>* row, int K, F&& f) {
   constexpr int V = BF16 ? 8 : 4;
   constexpr int ES = BF16 ? 2 : 4;
+  const int l = threadIdx.x;
   const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
-  int head = off ? (16 - off) / ES : 0;
-  if (head > K) head = K;
+  const int head = off ? (16 - off) / ES : 0;  // a wide row is longer than this
   const int nv = (K - head) / V, tail0 = head + nv * V;
-  if (lane < head || (lane >= 16 && tail0 + lane - 16 < K)) {
-    const int c = lane < 16 ? lane : tail0 + lane - 16;
+  if (l < head || (l >= 16 && tail0 + l - 16 < K)) {
+    const int c = l < 16 ? l : tail0 + l - 16;
     float v[V];
     if constexpr (BF16) v[0] = __bfloat162float(row[c]);
     else v[0] = row[c];
     f(v, c, 1);
   }
-  for (int i = lane; i < nv; i += 32) {
+  for (int i = l; i < nv; i += kThreads) {
     float v[V];
     const int c = head + i * V;
     if constexpr (BF16) {
@@ -67,145 +365,74 @@ __device__ __forceinline__ void for_row(const elem_t<BF16>* row, int K, int lane
   }
 }
 
-// counts[b][k] += picks of valid points; rows[b] += valid points.  Blocks of an
-// instance take its points round robin.
-__global__ void __launch_bounds__(kThreads) k_bal_count(const int32_t* __restrict__ idx,
-                                                        const uint8_t* __restrict__ valid, int64_t N, int K, int T,
-                                                        int nblk, int32_t* __restrict__ counts,
-                                                        int32_t* __restrict__ rows) {
-  extern __shared__ int32_t hist[];
-  const int b = blockIdx.x / nblk, blk = blockIdx.x - b * nblk;
-  const bool local = K <= kHistMax;
-  if (local) {
-    for (int k = threadIdx.x; k < K; k += kThreads) hist[k] = 0;
-    __syncthreads();
-  }
-  idx += b * N * T;
-  if (valid) valid += b * N;
-  counts += static_cast<int64_t>(b) * K;
-  int n = 0;
-  for (int64_t i = static_cast<int64_t>(blk) * kThreads + threadIdx.x; i < N; i += static_cast<int64_t>(nblk) * kThreads) {
-    if (valid && !valid[i]) continue;
-    ++n;
-    for (int t = 0; t < T; ++t) {
-      const int k = idx[i * T + t];
-      if (k >= 0 && k < K) atomicAdd(local ? &hist[k] : &counts[k], 1);
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  if ((threadIdx.x & 31) == 0 && n) atomicAdd(&rows[b], n);
-  if (local) {
-    __syncthreads();
-    for (int k = threadIdx.x; k < K; k += kThreads)
-      if (hist[k]) atomicAdd(&counts[k], hist[k]);
-  }
-}
-
-struct RowStat {
-  float m, s, t;  // running maximum, sum of exp(x - m), sum of f exp(x - m)
-};
-
-// One warp per row.
+// A block per row, running maxima and sums per thread.
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) k_bal_rows(const elem_t<BF16>* __restrict__ S,
-                                                       const uint8_t* __restrict__ valid, int64_t N, int K, int T,
-                                                       int nblk, const int32_t* __restrict__ counts,
-                                                       const int32_t* __restrict__ rows, float* __restrict__ lse,
-                                                       float* __restrict__ dot, double* __restrict__ part) {
-  __shared__ double wsum[kWarps];
-  const int b = blockIdx.x / nblk, blk = blockIdx.x - b * nblk;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t M = rows[b];
-  const float inv = M > 0 ? 1.f / (static_cast<float>(M) * static_cast<float>(T)) : 0.f;
-  const int32_t* cnt = counts + static_cast<int64_t>(b) * K;
+__global__ void __launch_bounds__(kThreads) k_bal_rows_wide(const elem_t<BF16>* __restrict__ S, const BalK p) {
+  constexpr int V = BF16 ? 8 : 4;
+  __shared__ float sm[3][kWarps];
+  const int b = blockIdx.x / p.nblk, blk = blockIdx.x - b * p.nblk;
+  pdl_wait();
+  const float inv = share_unit(p.rows[b], p.T);
+  const int32_t* cnt = p.counts + static_cast<int64_t>(b) * p.K;
   double sum = 0.0;
-  for (int64_t i = static_cast<int64_t>(blk) * kWarps + warp; i < N; i += static_cast<int64_t>(nblk) * kWarps) {
-    const int64_t o = b * N + i;
-    if (valid && !valid[o]) {
-      if (lane == 0) lse[o] = 0.f, dot[o] = 0.f;
-      continue;
-    }
-    RowStat st{-CUDART_INF_F, 0.f, 0.f};
-    for_row<BF16>(S + o * K, K, lane, [&](const auto& v, int c, int n) {
-      float m = st.m;
+  for (int64_t i = blk; i < p.N; i += p.nblk) {
+    const int64_t o = b * p.N + i;
+    const bool on = !p.valid || p.valid[o];
+    float m = -CUDART_INF_F, s = 0.f, t = 0.f;
+    if (on)
+      for_row<BF16>(S + o * p.K, p.K, [&](const float (&v)[V], int c, int n) {
+        float top = m;
 #pragma unroll
-      for (int j = 0; j < (BF16 ? 8 : 4); ++j)
-        if (j < n) m = fmaxf(m, v[j]);
-      const float sh = m == -CUDART_INF_F ? 0.f : m;  // a row so far all -inf: exp(-inf - 0) = 0
-      const float k = expf(st.m - sh);
-      st.s *= k;
-      st.t *= k;
-      st.m = m;
+        for (int j = 0; j < V; ++j)
+          if (j < n) top = fmaxf(top, v[j]);
+        const float sh = top == -CUDART_INF_F ? 0.f : top;  // so far all -inf: exp(-inf - 0) = 0
+        const float k = exp_of(m - sh);
+        s *= k;
+        t *= k;
+        m = top;
 #pragma unroll
-      for (int j = 0; j < (BF16 ? 8 : 4); ++j)
-        if (j < n) {
-          const float e = expf(v[j] - sh);
-          st.s += e;
-          st.t = fmaf(e, static_cast<float>(cnt[c + j]), st.t);
-        }
-    });
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) {
-      const float m2 = __shfl_xor_sync(0xffffffffu, st.m, s), s2 = __shfl_xor_sync(0xffffffffu, st.s, s);
-      const float t2 = __shfl_xor_sync(0xffffffffu, st.t, s);
-      const float m = fmaxf(st.m, m2), sh = m == -CUDART_INF_F ? 0.f : m;
-      const float k1 = expf(st.m - sh), k2 = expf(m2 - sh);
-      st.s = st.s * k1 + s2 * k2;
-      st.t = st.t * k1 + t2 * k2;
-      st.m = m;
-    }
-    // a row with nothing in it (all -inf) has no probabilities: r = 0
-    const float l = st.s == 0.f ? -CUDART_INF_F : (st.m == -CUDART_INF_F ? 0.f : st.m) + logf(st.s);
-    const float r = st.s == 0.f ? 0.f : st.t * inv / st.s;
-    if (lane == 0) {
-      lse[o] = l;
-      dot[o] = r;
-      sum += r;
+        for (int j = 0; j < V; ++j)
+          if (j < n) {
+            const float e = exp_of(v[j] - sh);
+            s += e;
+            t = fmaf(e, static_cast<float>(cnt[c + j]), t);
+          }
+      });
+    const float top = row_reduce<kThreads, true>(m, sm[0]);
+    const float sh = top == -CUDART_INF_F ? 0.f : top;
+    const float k = exp_of(m - sh);
+    s = row_reduce<kThreads, false>(s * k, sm[1]);
+    t = row_reduce<kThreads, false>(t * k, sm[2]);
+    if (threadIdx.x == 0) {
+      const RowNumbers n = on ? row_numbers(top, s, t * inv) : RowNumbers{0.f, 0.f};
+      p.lse[o] = n.lse;
+      p.dot[o] = n.r;
+      sum += n.r;
     }
   }
-  if (lane == 0) wsum[warp] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    double v = 0.0;
-    for (int w = 0; w < kWarps; ++w) v += wsum[w];
-    part[blockIdx.x] = v;
-  }
-}
-
-__global__ void __launch_bounds__(32) k_bal_loss(const double* __restrict__ part, int nblk, int K,
-                                                 const int32_t* __restrict__ rows, float* __restrict__ loss) {
-  const int b = blockIdx.x;
-  double v = 0.0;
-  for (int i = threadIdx.x; i < nblk; i += 32) v += part[static_cast<int64_t>(b) * nblk + i];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (threadIdx.x == 0) loss[b] = rows[b] > 0 ? static_cast<float>(v * K / rows[b]) : 0.f;
+  finish_loss(p, b, blk, sum);
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) k_bal_grad(const elem_t<BF16>* __restrict__ S,
-                                                       const uint8_t* __restrict__ valid, int64_t N, int K, int T,
-                                                       int nblk, const int32_t* __restrict__ counts,
-                                                       const int32_t* __restrict__ rows,
-                                                       const float* __restrict__ lse, const float* __restrict__ dot,
-                                                       const float* __restrict__ grad, elem_t<BF16>* __restrict__ dS) {
-  const int b = blockIdx.x / nblk, blk = blockIdx.x - b * nblk;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t M = rows[b];
-  const float inv = M > 0 ? 1.f / (static_cast<float>(M) * static_cast<float>(T)) : 0.f;
-  const float coef = M > 0 ? (grad ? grad[b] : 1.f) * static_cast<float>(K) / static_cast<float>(M) : 0.f;
-  const int32_t* cnt = counts + static_cast<int64_t>(b) * K;
-  for (int64_t i = static_cast<int64_t>(blk) * kWarps + warp; i < N; i += static_cast<int64_t>(nblk) * kWarps) {
-    const int64_t o = b * N + i;
-    const float l = lse[o], r = dot[o];
-    const bool none = (valid && !valid[o]) || l == -CUDART_INF_F;
-    elem_t<BF16>* out = dS + o * K;
-    for_row<BF16>(S + o * K, K, lane, [&](const auto& v, int c, int n) {
-      float d[BF16 ? 8 : 4];
+__global__ void __launch_bounds__(kThreads) k_bal_grad_wide(const elem_t<BF16>* __restrict__ S,
+                                                            elem_t<BF16>* __restrict__ dS, const BalK p) {
+  constexpr int V = BF16 ? 8 : 4;
+  const int b = blockIdx.x / p.nblk, blk = blockIdx.x - b * p.nblk;
+  const int64_t M = p.rows[b];
+  const float inv = share_unit(M, p.T);
+  const float coef = M > 0 ? (p.grad ? p.grad[b] : 1.f) * static_cast<float>(p.K) / static_cast<float>(M) : 0.f;
+  const int32_t* cnt = p.counts + static_cast<int64_t>(b) * p.K;
+  for (int64_t i = blk; i < p.N; i += p.nblk) {
+    const int64_t o = b * p.N + i;
+    const float ls = p.lse[o], r = p.dot[o];
+    const bool on = (!p.valid || p.valid[o]) && ls != -CUDART_INF_F;
+    elem_t<BF16>* out = dS + o * p.K;
+    for_row<BF16>(S + o * p.K, p.K, [&](const float (&v)[V], int c, int n) {
+      float d[V];
 #pragma unroll
-      for (int j = 0; j < (BF16 ? 8 : 4); ++j)
-        if (j < n) d[j] = none ? 0.f : coef * expf(v[j] - l) * (static_cast<float>(cnt[c + j]) * inv - r);
+      for (int j = 0; j < V; ++j)
+        d[j] = on && j < n
+                   ? coef * exp_of(v[j] - ls) * (static_cast<float>(cnt[c + j]) * inv - r) : 0.f;
       if (n == 1) {
         if constexpr (BF16) out[c] = __float2bfloat16_rn(d[0]);
         else out[c] = d[0];
@@ -224,61 +451,154 @@ __global__ void __launch_bounds__(kThreads) k_bal_grad(const elem_t<BF16>* __res
   }
 }
 
-cudaError_t plain_launch() {
+// ------------------------------------------------------------------- launches
+// Threads per row: 16-byte chunks, four per thread, else single elements, as
+// few per thread as 32 threads allow.  0: a wide row.
+struct RowForm {
+  bool vec;
+  int lpr, nc;
+};
+RowForm row_form(int K, int dtype) {
+  const int es = dtype == kDtypeBF16 ? 2 : 4, v = 16 / es;
+  RowForm r{};
+  r.vec = K % v == 0;
+  const int chunks = r.vec ? K / v : K;
+  if (r.vec) {
+    r.nc = 4;
+    r.lpr = 1;
+    while (r.lpr * r.nc < chunks) r.lpr *= 2;
+  } else {
+    r.lpr = 32;
+    r.nc = 1;
+    while (r.nc < kRegCols && r.lpr * r.nc < chunks) r.nc *= 2;
+    while (r.lpr * r.nc < chunks) r.lpr *= 2;
+  }
+  if (r.lpr > kThreads) r.lpr = 0;
+  return r;
+}
+int rows_per_block(int K, int dtype) {
+  const RowForm r = row_form(K, dtype);
+  return r.lpr ? kThreads / r.lpr : 1;
+}
+
+// Calls go(LPR, NC) with the form's compile-time sizes.
+template <typename Go>
+void with_form(const RowForm& r, Go&& go) {
+  auto c = [](auto x) { return x; };
+  using std::integral_constant;
+#define KM_CASE(L, N) \
+  if (r.lpr == L && r.nc == N) return go(c(integral_constant<int, L>{}), c(integral_constant<int, N>{}));
+  if (r.vec) {
+    KM_CASE(1, 4) KM_CASE(2, 4) KM_CASE(4, 4) KM_CASE(8, 4) KM_CASE(16, 4) KM_CASE(32, 4) KM_CASE(64, 4)
+    KM_CASE(128, 4) KM_CASE(256, 4)
+  } else {
+    KM_CASE(32, 1) KM_CASE(32, 2) KM_CASE(32, 4) KM_CASE(32, 8) KM_CASE(32, 16) KM_CASE(32, 32) KM_CASE(64, 32)
+    KM_CASE(128, 32) KM_CASE(256, 32)
+  }
+#undef KM_CASE
+}
+
+BalK make_k(const BalanceArgs& a) {
+  BalK k{};
+  k.idx = a.idx;
+  k.valid = a.valid;
+  k.N = a.N;
+  k.K = a.K;
+  k.T = a.T;
+  k.nblk = balance_blocks(a.B, a.N, a.K, a.dtype);
+  k.loss = a.loss;
+  k.counts = a.counts;
+  k.rows = a.rows;
+  k.lse = a.lse;
+  k.dot = a.dot;
+  k.part = a.part;
+  k.done = a.done;
+  k.grad = a.grad;
+  return k;
+}
+
+template <bool BF16>
+cudaError_t rows_launch(const BalanceArgs& a, const BalK& k, cudaStream_t s) {
+  using T = elem_t<BF16>;
+  const T* S = static_cast<const T*>(a.S);
+  const dim3 grid(static_cast<unsigned>(k.nblk) * a.B);
+  const RowForm r = row_form(a.K, a.dtype);
+  cudaError_t e = cudaErrorInvalidValue;
+  count_launch();
+  if (!r.lpr) return launch_chained(k_bal_rows_wide<BF16>, grid, dim3(kThreads), 0, s, S, k);
+  with_form(r, [&](auto L, auto N) {
+    e = r.vec ? launch_chained(k_bal_rows<BF16, true, L(), (N() > 4 ? 4 : N())>, grid, dim3(kThreads), 0, s, S, k)
+              : launch_chained(k_bal_rows<BF16, false, (L() < 32 ? 32 : L()), N()>, grid, dim3(kThreads), 0, s, S, k);
+  });
+  return e;
+}
+
+template <bool BF16>
+cudaError_t grad_launch(const BalanceArgs& a, const BalK& k, cudaStream_t s) {
+  using T = elem_t<BF16>;
+  const T* S = static_cast<const T*>(a.S);
+  T* dS = static_cast<T*>(a.dS);
+  const unsigned grid = static_cast<unsigned>(k.nblk) * a.B;
+  const RowForm r = row_form(a.K, a.dtype);
   chain_break();
   if (fault_hit(kFaultLaunch)) return cudaErrorLaunchFailure;
   count_launch();
-  return cudaSuccess;
+  if (!r.lpr) {
+    k_bal_grad_wide<BF16><<<grid, kThreads, 0, s>>>(S, dS, k);
+  } else {
+    with_form(r, [&](auto L, auto N) {
+      if (r.vec) k_bal_grad<BF16, true, L(), (N() > 4 ? 4 : N())><<<grid, kThreads, 0, s>>>(S, dS, k);
+      else k_bal_grad<BF16, false, (L() < 32 ? 32 : L()), N()><<<grid, kThreads, 0, s>>>(S, dS, k);
+    });
+  }
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 // Blocks per instance of the row passes: the device a few times over, at least
-// eight rows (one per warp) each.
-int balance_blocks(int B, int64_t N) {
+// two rounds of rows each.
+int balance_blocks(int B, int64_t N, int K, int dtype) {
+  const int rpb = rows_per_block(K, dtype);
   int64_t n = (148 * 8 + B - 1) / B;
-  const int64_t most = (N + kWarps - 1) / kWarps;
+  const int64_t most = (N + 2 * rpb - 1) / (2 * rpb);
   if (n > most) n = most;
   return static_cast<int>(n < 1 ? 1 : n);
 }
 
 cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t s) {
-  cudaError_t e = cudaMemsetAsync(a.counts, 0, sizeof(int32_t) * static_cast<size_t>(a.B) * a.K, s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(a.rows, 0, sizeof(int32_t) * a.B, s);
-  if (e != cudaSuccess) return e;
-  const int nblk = balance_blocks(a.B, a.N);
-  const unsigned grid = static_cast<unsigned>(nblk) * a.B;
-  if ((e = plain_launch()) != cudaSuccess) return e;
+  const BalK k = make_k(a);
+  cudaError_t e;
+  // One block counts a small instance alone; more of them add to zeroed counts.
+  const int64_t picks = a.N * a.T;
+  const bool solo = picks <= 16384 && a.K <= kHistMax;
   const size_t sm = a.K <= kHistMax ? sizeof(int32_t) * a.K : 0;
-  k_bal_count<<<grid, kThreads, sm, s>>>(a.idx, a.valid, a.N, a.K, a.T, nblk, a.counts, a.rows);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if ((e = plain_launch()) != cudaSuccess) return e;
-  if (a.dtype == kDtypeBF16)
-    k_bal_rows<true><<<grid, kThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(a.S), a.valid, a.N, a.K, a.T, nblk,
-                                               a.counts, a.rows, a.lse, a.dot, a.part);
-  else
-    k_bal_rows<false><<<grid, kThreads, 0, s>>>(static_cast<const float*>(a.S), a.valid, a.N, a.K, a.T, nblk, a.counts,
-                                                a.rows, a.lse, a.dot, a.part);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if ((e = plain_launch()) != cudaSuccess) return e;
-  k_bal_loss<<<a.B, 32, 0, s>>>(a.part, nblk, a.K, a.rows, a.loss);
-  return cudaGetLastError();
+  if (solo) {
+    count_launch();
+    e = launch_chained(k_bal_count<true>, dim3(a.B), dim3(kThreads), sm, s, k, 1);
+  } else {
+    const int64_t nc = static_cast<int64_t>(a.B) * a.K;
+    const int64_t zb = (nc + kThreads - 1) / kThreads, mb = (a.B + kThreads - 1) / kThreads;
+    const unsigned zgrid = static_cast<unsigned>(zb > 296 ? (mb > 296 ? mb : 296) : zb);
+    count_launch();
+    e = launch_chained(k_bal_zero, dim3(zgrid), dim3(kThreads), 0, s, k, nc, a.B);
+    if (e != cudaSuccess) return e;
+    int64_t nblk = (148 * 4 + a.B - 1) / a.B;
+    const int64_t most = (picks + 2047) / 2048;
+    if (nblk > most) nblk = most;
+    if (nblk < 1) nblk = 1;
+    count_launch();
+    e = launch_chained(k_bal_count<false>, dim3(static_cast<unsigned>(nblk) * a.B), dim3(kThreads), sm, s, k,
+                       static_cast<int>(nblk));
+  }
+  if (e != cudaSuccess) return e;
+  return a.dtype == kDtypeBF16 ? rows_launch<true>(a, k, s) : rows_launch<false>(a, k, s);
 }
 
 cudaError_t launch_balance_grad(const BalanceArgs& a, cudaStream_t s) {
   if (a.N == 0) return cudaSuccess;
-  const int nblk = balance_blocks(a.B, a.N);
-  const unsigned grid = static_cast<unsigned>(nblk) * a.B;
-  cudaError_t e = plain_launch();
-  if (e != cudaSuccess) return e;
-  if (a.dtype == kDtypeBF16)
-    k_bal_grad<true><<<grid, kThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(a.S), a.valid, a.N, a.K, a.T, nblk,
-                                               a.counts, a.rows, a.lse, a.dot, a.grad,
-                                               static_cast<__nv_bfloat16*>(a.dS));
-  else
-    k_bal_grad<false><<<grid, kThreads, 0, s>>>(static_cast<const float*>(a.S), a.valid, a.N, a.K, a.T, nblk, a.counts,
-                                                a.rows, a.lse, a.dot, a.grad, static_cast<float*>(a.dS));
-  return cudaGetLastError();
+  const BalK k = make_k(a);
+  return a.dtype == kDtypeBF16 ? grad_launch<true>(a, k, s) : grad_launch<false>(a, k, s);
 }
 
 }  // namespace km

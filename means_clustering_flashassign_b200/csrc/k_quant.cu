@@ -11,7 +11,8 @@
 // smallest value, 2^-9 * 2^e, a normal bf16.  A block holding an infinity or
 // a NaN gets the NaN scale (255): every value it stands for is NaN.
 //
-// Both directions are one pass over memory.
+// Both directions are one pass over memory; a thread has the loads of four
+// pieces in flight before it uses the first.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -61,47 +62,59 @@ __device__ __forceinline__ void load_coords(const elem_t<BF16>* row, int c0, int
   }
 }
 
+constexpr int kU = 4;  // pieces in flight per thread
+
 // LPB lanes (a power of two, at most 16) hold one block of 8 * LPB >= 128 or
-// >= D coordinates; rows * nb blocks in all.
-template <bool BF16, bool VEC, int LPB>
-__global__ void __launch_bounds__(kQThreads) k_quantize(const elem_t<BF16>* __restrict__ X, int64_t blocks, int nb, int D,
+// >= D coordinates; rows * nb blocks in all.  I is the type block numbers fit
+// (a 64-bit division per block is slower than the block's arithmetic).
+template <bool BF16, bool VEC, int LPB, typename I>
+__global__ void __launch_bounds__(kQThreads) k_quantize(const elem_t<BF16>* __restrict__ X, I blocks, int nb, int D,
                                                         int64_t ld, uint8_t* __restrict__ q,
                                                         uint8_t* __restrict__ scale) {
+  constexpr I kPer = kQThreads / LPB;  // blocks of one piece
   const int l = threadIdx.x % LPB;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kQThreads / LPB);
+  const I step = static_cast<I>(gridDim.x) * (kPer * kU);
   // every lane of a warp runs the same number of rounds: the shuffles below
   // take the whole warp
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kQThreads / LPB);
-  for (int64_t base = first; base < blocks; base += step) {
-    const int64_t blk = base + threadIdx.x / LPB;
-    const bool on = blk < blocks;
-    const int64_t row = on ? blk / nb : 0;
-    const int c0 = static_cast<int>(on ? blk - row * nb : 0) * kQBlock + l * kE;
-    float v[kE];
-    load_coords<BF16, VEC>(X + row * D, on ? c0 : D, D, v);
-    uint32_t a = 0;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * (kPer * kU); base < static_cast<int64_t>(blocks); base += step) {
+    float v[kU][kE];
+    int64_t row[kU];
+    int c0[kU];
 #pragma unroll
-    for (int i = 0; i < kE; ++i) a = max(a, __float_as_uint(v[i]) & 0x7fffffffu);
-#pragma unroll
-    for (int o = LPB / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-    // a = f * 2^k with f in [0.5, 1): a <= 448 * 2^e = 0.875 * 2^(e + 9) needs
-    // e >= k - 9, one more if f > 0.875 (fraction bits above .75 of the last octave)
-    int e = static_cast<int>(a >> 23) - 126 - 9 + ((a & 0x7fffffu) > 0x600000u ? 1 : 0);
-    e = max(e, -117);
-    const bool bad = a >= 0x7f800000u;  // an infinity or a NaN
-    const float inv = bad ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    if (!on) continue;
-    uint32_t w[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h] * inv, v[4 * h + 1] * inv), __NV_SATFINITE,
-                                                   __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h + 2] * inv, v[4 * h + 3] * inv),
-                                                   __NV_SATFINITE, __NV_E4M3);
-      w[h] = lo | (hi << 16);
+    for (int u = 0; u < kU; ++u) {
+      const int64_t at = base + u * kPer + threadIdx.x / LPB;
+      const bool on = at < static_cast<int64_t>(blocks);
+      const I blk = on ? static_cast<I>(at) : 0, r = nb == 1 ? blk : blk / static_cast<I>(nb);
+      row[u] = on ? static_cast<int64_t>(r) : -1;
+      c0[u] = static_cast<int>(blk - r * static_cast<I>(nb)) * kQBlock + l * kE;
+      load_coords<BF16, VEC>(X + static_cast<int64_t>(r) * D, on ? c0[u] : D, D, v[u]);
     }
-    if (c0 < ld) *reinterpret_cast<uint2*>(q + row * ld + c0) = make_uint2(w[0], w[1]);
-    if (l == 0) scale[blk] = bad ? 255 : static_cast<uint8_t>(e + 127);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      uint32_t a = 0;
+#pragma unroll
+      for (int i = 0; i < kE; ++i) a = max(a, __float_as_uint(v[u][i]) & 0x7fffffffu);
+#pragma unroll
+      for (int o = LPB / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+      // a = f * 2^k with f in [0.5, 1): a <= 448 * 2^e = 0.875 * 2^(e + 9) needs
+      // e >= k - 9, one more if f > 0.875 (fraction bits above .75 of the last octave)
+      int e = static_cast<int>(a >> 23) - 126 - 9 + ((a & 0x7fffffu) > 0x600000u ? 1 : 0);
+      e = max(e, -117);
+      const bool bad = a >= 0x7f800000u;  // an infinity or a NaN
+      const float inv = bad ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      if (row[u] < 0) continue;
+      uint32_t w[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[u][4 * h] * inv, v[u][4 * h + 1] * inv),
+                                                     __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[u][4 * h + 2] * inv, v[u][4 * h + 3] * inv),
+                                                     __NV_SATFINITE, __NV_E4M3);
+        w[h] = lo | (hi << 16);
+      }
+      if (c0[u] < ld) *reinterpret_cast<uint2*>(q + row[u] * ld + c0[u]) = make_uint2(w[0], w[1]);
+      if (l == 0) scale[row[u] * nb + c0[u] / kQBlock] = bad ? 255 : static_cast<uint8_t>(e + 127);
+    }
   }
 }
 
@@ -110,48 +123,71 @@ __device__ __forceinline__ float e8m0(uint32_t b) {
   return __uint_as_float(b == 255u ? 0x7fc00000u : (b ? b << 23 : 0x00400000u));
 }
 
-// kE coordinates per thread; rows of q hold ld / kE such groups.
-template <bool BF16, bool VEC>
+constexpr int kDE = 16;  // coordinates per piece of k_dequantize: 16 bytes of q
+constexpr int kDU = 2;
+
+// gpr pieces per row.
+template <bool BF16, bool VEC, typename I>
 __global__ void __launch_bounds__(kQThreads) k_dequantize(const uint8_t* __restrict__ q,
-                                                          const uint8_t* __restrict__ scale, int64_t groups, int gpr,
-                                                          int nb, int D, int64_t ld, int64_t ld_out,
+                                                          const uint8_t* __restrict__ scale, I groups, int gpr, int nb,
+                                                          int D, int64_t ld, int64_t ld_out,
                                                           elem_t<BF16>* __restrict__ X) {
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kQThreads;
-  for (int64_t g = static_cast<int64_t>(blockIdx.x) * kQThreads + threadIdx.x; g < groups; g += step) {
-    const int64_t row = g / gpr;
-    const int c0 = static_cast<int>(g - row * gpr) * kE;
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(q + row * ld + c0));
-    const float s = e8m0(__ldg(scale + row * nb + c0 / kQBlock));
-    float v[kE];
-    const uint32_t w[2] = {u.x, u.y};
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kQThreads * kDU);
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * (kQThreads * kDU) + threadIdx.x;
+       base < static_cast<int64_t>(groups); base += step) {
+    uint4 u[kDU];
+    float s[kDU];
+    int64_t row[kDU];
+    int c0[kDU];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i / 2] >> (16 * (i & 1))),
-                                                       __NV_E4M3);
-      const float2 f = __half22float2(__half2(h));
-      v[2 * i] = f.x * s;
-      v[2 * i + 1] = f.y * s;
+    for (int k = 0; k < kDU; ++k) {
+      const int64_t at = base + k * kQThreads;
+      const bool on = at < static_cast<int64_t>(groups);
+      const I g = on ? static_cast<I>(at) : 0, r = g / static_cast<I>(gpr);
+      row[k] = on ? static_cast<int64_t>(r) : -1;
+      c0[k] = static_cast<int>(g - r * static_cast<I>(gpr)) * kDE;
+      u[k] = __ldg(reinterpret_cast<const uint4*>(q + static_cast<int64_t>(r) * ld + c0[k]));
+      s[k] = e8m0(__ldg(scale + static_cast<int64_t>(r) * nb + c0[k] / kQBlock));
     }
-    elem_t<BF16>* out = X + row * ld_out + c0;
-    if (VEC) {
-      if constexpr (BF16) {
-        uint32_t o[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-          o[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        if (c0 < D) *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
-      } else if (c0 < D) {
-        reinterpret_cast<float4*>(out)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(out)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    for (int k = 0; k < kDU; ++k) {
+      if (row[k] < 0) continue;
+      float v[kDE];
+      const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+      for (int i = 0; i < kDE / 2; ++i) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+            static_cast<__nv_fp8x2_storage_t>(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
+        const float2 f = __half22float2(__half2(h));
+        v[2 * i] = f.x * s[k];
+        v[2 * i + 1] = f.y * s[k];
       }
-    } else {
+      elem_t<BF16>* out = X + row[k] * ld_out + c0[k];
+      if (VEC) {
 #pragma unroll
-      for (int i = 0; i < kE; ++i) {
-        if (c0 + i >= D) break;
-        if constexpr (BF16) out[i] = __float2bfloat16_rn(v[i]);
-        else out[i] = v[i];
+        for (int h = 0; h < 2; ++h) {  // 8 coordinates; D and the rows are multiples of 8
+          if (c0[k] + 8 * h >= D) break;
+          if constexpr (BF16) {
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[8 * h + 2 * i], v[8 * h + 2 * i + 1]);
+              o[i] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+            reinterpret_cast<uint4*>(out)[h] = make_uint4(o[0], o[1], o[2], o[3]);
+          } else {
+            reinterpret_cast<float4*>(out)[2 * h] = make_float4(v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3]);
+            reinterpret_cast<float4*>(out)[2 * h + 1] =
+                make_float4(v[8 * h + 4], v[8 * h + 5], v[8 * h + 6], v[8 * h + 7]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kDE; ++i) {
+          if (c0[k] + i >= D) break;
+          if constexpr (BF16) out[i] = __float2bfloat16_rn(v[i]);
+          else out[i] = v[i];
+        }
       }
     }
   }
@@ -165,8 +201,12 @@ unsigned grid_for(int64_t units, int64_t per_block) {
 
 template <bool BF16, bool VEC, int LPB>
 void quantize_t(const void* X, int64_t blocks, int nb, int D, uint8_t* q, uint8_t* scale, cudaStream_t s) {
-  k_quantize<BF16, VEC, LPB><<<grid_for(blocks, kQThreads / LPB), kQThreads, 0, s>>>(
-      static_cast<const elem_t<BF16>*>(X), blocks, nb, D, q_ld(D), q, scale);
+  const unsigned grid = grid_for(blocks, kQThreads / LPB * kU);
+  const auto* x = static_cast<const elem_t<BF16>*>(X);
+  if (blocks < (int64_t(1) << 31))
+    k_quantize<BF16, VEC, LPB, uint32_t><<<grid, kQThreads, 0, s>>>(x, static_cast<uint32_t>(blocks), nb, D, q_ld(D), q, scale);
+  else
+    k_quantize<BF16, VEC, LPB, int64_t><<<grid, kQThreads, 0, s>>>(x, blocks, nb, D, q_ld(D), q, scale);
 }
 
 template <bool BF16, bool VEC>
@@ -176,6 +216,19 @@ void quantize_d(const void* X, int64_t blocks, int nb, int D, uint8_t* q, uint8_
   else if (D > 32) quantize_t<BF16, VEC, 8>(X, blocks, nb, D, q, scale, s);
   else if (D > 16) quantize_t<BF16, VEC, 4>(X, blocks, nb, D, q, scale, s);
   else quantize_t<BF16, VEC, 2>(X, blocks, nb, D, q, scale, s);
+}
+
+template <bool BF16, bool VEC>
+void dequantize_t(const uint8_t* q, const uint8_t* scale, int64_t rows, int D, int64_t ld_out, void* X, cudaStream_t s) {
+  const int gpr = (D + kDE - 1) / kDE;
+  const int64_t groups = rows * gpr;
+  const unsigned grid = grid_for(groups, kQThreads * kDU);
+  auto* o = static_cast<elem_t<BF16>*>(X);
+  if (groups < (int64_t(1) << 31))
+    k_dequantize<BF16, VEC, uint32_t><<<grid, kQThreads, 0, s>>>(q, scale, static_cast<uint32_t>(groups), gpr, q_blocks(D),
+                                                                 D, q_ld(D), ld_out, o);
+  else
+    k_dequantize<BF16, VEC, int64_t><<<grid, kQThreads, 0, s>>>(q, scale, groups, gpr, q_blocks(D), D, q_ld(D), ld_out, o);
 }
 
 }  // namespace
@@ -201,21 +254,11 @@ cudaError_t launch_dequantize(const uint8_t* q, const uint8_t* scale, int dtype,
   chain_break();
   if (fault_hit(kFaultLaunch)) return cudaErrorLaunchFailure;
   count_launch();
-  const int nb = q_blocks(D);
-  const int gpr = (D + kE - 1) / kE;
-  const int64_t groups = rows * gpr, ld = q_ld(D);
-  const unsigned grid = grid_for(groups, kQThreads);
-  const bool bf16 = dtype == kDtypeBF16;
   const bool vec = D % 8 == 0 && ld_out % 8 == 0 && reinterpret_cast<uintptr_t>(X) % 16 == 0;
-  if (bf16) {
-    auto* o = static_cast<__nv_bfloat16*>(X);
-    if (vec) k_dequantize<true, true><<<grid, kQThreads, 0, s>>>(q, scale, groups, gpr, nb, D, ld, ld_out, o);
-    else k_dequantize<true, false><<<grid, kQThreads, 0, s>>>(q, scale, groups, gpr, nb, D, ld, ld_out, o);
-  } else {
-    auto* o = static_cast<float*>(X);
-    if (vec) k_dequantize<false, true><<<grid, kQThreads, 0, s>>>(q, scale, groups, gpr, nb, D, ld, ld_out, o);
-    else k_dequantize<false, false><<<grid, kQThreads, 0, s>>>(q, scale, groups, gpr, nb, D, ld, ld_out, o);
-  }
+  if (dtype == kDtypeBF16)
+    vec ? dequantize_t<true, true>(q, scale, rows, D, ld_out, X, s) : dequantize_t<true, false>(q, scale, rows, D, ld_out, X, s);
+  else
+    vec ? dequantize_t<false, true>(q, scale, rows, D, ld_out, X, s) : dequantize_t<false, false>(q, scale, rows, D, ld_out, X, s);
   return cudaGetLastError();
 }
 

@@ -54,7 +54,7 @@ int check_shape(int B, int64_t N, int D, int K, int dtype) {
 
 // Workspace layout of an operator (offsets in bytes; the status word is at 0).
 struct Layout {
-  size_t off_cop = 0, off_xop = 0, off_planes = 0, off_parts = 0, off_cols = 0, off_bal = 0, total = 0;
+  size_t off_cop = 0, off_xop = 0, off_planes = 0, off_parts = 0, off_cols = 0, off_bal = 0, off_done = 0, total = 0;
   int planes = 1;
   bool copy_ds = false;
   GradPlan gp{};
@@ -83,7 +83,8 @@ int make_layout(Layout& l, int op, int B, int64_t N, int D, int K, int dtype) {
     if (l.gp.splits > 1) l.off_parts = take(sizeof(float) * l.gp.splits * static_cast<size_t>(B) * K * D);
     l.off_cols = take(sizeof(float) * l.gp.splits * l.gp.parts * static_cast<size_t>(B) * K);
   } else if (op == KM_SOFT_BALANCE) {
-    l.off_bal = take(sizeof(double) * static_cast<size_t>(B) * balance_blocks(B, N));
+    l.off_bal = take(sizeof(double) * static_cast<size_t>(B) * balance_blocks(B, N, K, dtype));
+    l.off_done = take(sizeof(unsigned int) * static_cast<size_t>(B));
   }
   l.total = off;
   return KM_OK;
@@ -287,6 +288,7 @@ int km_balance(const void* S, const int32_t* idx, const uint8_t* valid, int B, i
   a.lse = lse;
   a.dot = dot;
   a.part = reinterpret_cast<double*>(c.ws + c.l.off_bal);
+  a.done = reinterpret_cast<unsigned int*>(c.ws + c.l.off_done);
   SOFT_CUDA(launch_balance(a, c.s));
   return KM_OK;
 }

@@ -106,12 +106,13 @@ struct BalanceArgs {
   int32_t* rows;
   float* lse;
   float* dot;
-  double* part;  // [B][balance_blocks]
+  double* part;        // [B][balance_blocks]
+  unsigned int* done;  // [B]
   // gradient only
   const float* grad;  // [B] or null (1)
   void* dS;
 };
-int balance_blocks(int B, int64_t N);
+int balance_blocks(int B, int64_t N, int K, int dtype);
 cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t s);
 cudaError_t launch_balance_grad(const BalanceArgs& a, cudaStream_t s);
 
