@@ -43,10 +43,10 @@ using elem_t = typename std::conditional<BF16, __nv_bfloat16, float>::type;
 // exp(x) for x <= 0 (or NaN): 2^(x log2 e), whose rounded argument is off by
 // |x| 2^-24 -- no more than x, a difference of two float32 scores, is itself.
 // The difference comes first: a score near the type's lowest value times log2 e
-// would overflow.
+// would overflow.  Results below 2^-126 are 0, beside a largest term of 1.
 __device__ __forceinline__ float exp_of(float x) {
   float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x * kLog2e));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * kLog2e));
   return y;
 }
 
@@ -122,6 +122,15 @@ template <bool BF16, bool VEC, int NC>
 struct Raw {
   using Word = typename std::conditional<VEC, uint4, typename std::conditional<BF16, uint16_t, uint32_t>::type>::type;
   Word w[NC];
+  // All -inf: words behind the row's end are never loaded and stay so.
+  __device__ __forceinline__ Raw() {
+    constexpr uint32_t kInf = BF16 ? 0xff80ff80u : 0xff800000u;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      if constexpr (VEC) w[j] = make_uint4(kInf, kInf, kInf, kInf);
+      else w[j] = static_cast<Word>(kInf);
+    }
+  }
 };
 
 template <bool BF16, bool VEC, int LPR, int NC>
@@ -135,28 +144,26 @@ __device__ __forceinline__ void load_raw(Raw<BF16, VEC, NC>& r, const elem_t<BF1
   }
 }
 
-// The columns' values (-inf behind the row's end).
-template <bool BF16, bool VEC, int LPR, int NC, int E>
-__device__ __forceinline__ void unpack_raw(const Raw<BF16, VEC, NC>& r, int K, int l, float (&x)[E]) {
+template <bool BF16, bool VEC, int NC, int E>
+__device__ __forceinline__ void unpack_raw(const Raw<BF16, VEC, NC>& r, float (&x)[E]) {
   constexpr int V = VEC ? (BF16 ? 8 : 4) : 1;
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
-    const bool in = (j * LPR + l) * V < K;
     if constexpr (VEC) {
       const uint32_t w[4] = {r.w[j].x, r.w[j].y, r.w[j].z, r.w[j].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (BF16) {
-          x[j * V + 2 * i] = in ? __uint_as_float(w[i] << 16) : -CUDART_INF_F;
-          x[j * V + 2 * i + 1] = in ? __uint_as_float(w[i] & 0xffff0000u) : -CUDART_INF_F;
+          x[j * V + 2 * i] = __uint_as_float(w[i] << 16);
+          x[j * V + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         } else {
-          x[j * V + i] = in ? __uint_as_float(w[i]) : -CUDART_INF_F;
+          x[j * V + i] = __uint_as_float(w[i]);
         }
       }
     } else if constexpr (BF16) {
-      x[j] = in ? __uint_as_float(static_cast<uint32_t>(r.w[j]) << 16) : -CUDART_INF_F;
+      x[j] = __uint_as_float(static_cast<uint32_t>(r.w[j]) << 16);
     } else {
-      x[j] = in ? __uint_as_float(r.w[j]) : -CUDART_INF_F;
+      x[j] = __uint_as_float(r.w[j]);
     }
   }
 }
@@ -249,12 +256,12 @@ __global__ void __launch_bounds__(kThreads) k_bal_rows(const elem_t<BF16>* __res
   int64_t i = static_cast<int64_t>(blk) * RPB + threadIdx.x / LPR;
   auto usable = [&](int64_t r) { return r < p.N && (!p.valid || p.valid[b * p.N + r]); };
   bool on = usable(i);
-  Raw<BF16, VEC, NC> next{};
+  Raw<BF16, VEC, NC> next;
   load_raw<BF16, VEC, LPR, NC>(next, S + (b * p.N + i) * p.K, p.K, l, on);
   // every thread of the block runs the same rounds (the reductions may span it)
   for (int64_t base = static_cast<int64_t>(blk) * RPB; base < p.N; base += step, i += step) {
     float x[E];
-    unpack_raw<BF16, VEC, LPR, NC, E>(next, p.K, l, x);
+    unpack_raw<BF16, VEC, NC, E>(next, x);
     const bool now = on;
     on = usable(i + step);
     load_raw<BF16, VEC, LPR, NC>(next, S + (b * p.N + i + step) * p.K, p.K, l, on);
@@ -283,7 +290,7 @@ __global__ void __launch_bounds__(kThreads) k_bal_rows(const elem_t<BF16>* __res
 }
 
 template <bool BF16, bool VEC, int LPR, int NC>
-__global__ void __launch_bounds__(kThreads) k_bal_grad(const elem_t<BF16>* __restrict__ S,
+__global__ void __launch_bounds__(kThreads, 3) k_bal_grad(const elem_t<BF16>* __restrict__ S,
                                                        elem_t<BF16>* __restrict__ dS, const BalK p) {
   constexpr int V = VEC ? (BF16 ? 8 : 4) : 1, E = NC * V, RPB = kThreads / LPR;
   const int b = blockIdx.x / p.nblk, blk = blockIdx.x - b * p.nblk;
@@ -292,17 +299,25 @@ __global__ void __launch_bounds__(kThreads) k_bal_grad(const elem_t<BF16>* __res
   const float coef = M > 0 ? (p.grad ? p.grad[b] : 1.f) * static_cast<float>(p.K) / static_cast<float>(M) : 0.f;
   float f[E];
   load_shares<V, LPR, NC, E>(p.counts + static_cast<int64_t>(b) * p.K, p.K, l, share_unit(M, p.T), f);
+#pragma unroll
+  for (int j = 0; j < E; ++j) f[j] *= coef;
+  Raw<BF16, VEC, NC> raw;
   const int64_t step = static_cast<int64_t>(p.nblk) * RPB;
   for (int64_t i = static_cast<int64_t>(blk) * RPB + threadIdx.x / LPR; i < p.N; i += step) {
     const int64_t o = b * p.N + i;
     const float ls = p.lse[o], r = p.dot[o];
     const bool on = (!p.valid || p.valid[o]) && ls != -CUDART_INF_F;
-    Raw<BF16, VEC, NC> raw{};
-    load_raw<BF16, VEC, LPR, NC>(raw, S + o * p.K, p.K, l, on);
     float x[E];
-    unpack_raw<BF16, VEC, LPR, NC, E>(raw, p.K, l, x);
-    #pragma unroll
-    for (int j = 0; j < E; ++j) x[j] = on ? coef * exp_of(x[j] - ls) * (f[j] - r) : 0.f;
+    if (on) {
+      load_raw<BF16, VEC, LPR, NC>(raw, S + o * p.K, p.K, l, true);
+      unpack_raw<BF16, VEC, NC, E>(raw, x);
+      const float rc = r * coef;
+#pragma unroll
+      for (int j = 0; j < E; ++j) x[j] = exp_of(x[j] - ls) * (f[j] - rc);
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) x[j] = 0.f;
+    }
     elem_t<BF16>* out = dS + o * p.K;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {

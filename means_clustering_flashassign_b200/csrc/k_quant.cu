@@ -26,74 +26,97 @@ namespace km {
 namespace {
 
 constexpr int kQThreads = 256;
-constexpr int kE = 8;  // coordinates per lane
+constexpr int kE = 16;  // coordinates per lane of k_quantize
 
 template <bool BF16>
 using elem_t = typename std::conditional<BF16, __nv_bfloat16, float>::type;
 
-__device__ __forceinline__ float bf16_bits(uint32_t h) { return __uint_as_float(h << 16); }
-
-// kE coordinates from c0 of a row (those at or beyond D read as 0).
-template <bool BF16, bool VEC>
-__device__ __forceinline__ void load_coords(const elem_t<BF16>* row, int c0, int D, float (&v)[kE]) {
-  if (VEC) {  // D % 8 == 0 and 16-byte rows: all or nothing
-    if (c0 >= D) {
-#pragma unroll
-      for (int i = 0; i < kE; ++i) v[i] = 0.f;
-    } else if constexpr (BF16) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + c0));
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16_bits(w[i] & 0xffffu);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
-    } else {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(row + c0));
-      const float4 b = __ldg(reinterpret_cast<const float4*>(row + c0) + 1);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kE; ++i) {
-      if constexpr (BF16) v[i] = c0 + i < D ? __bfloat162float(row[c0 + i]) : 0.f;
-      else v[i] = c0 + i < D ? row[c0 + i] : 0.f;
-    }
-  }
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
-constexpr int kU = 4;  // pieces in flight per thread
+// kE coordinates from c0 of a row (those at or beyond D as 0): bf16 two to a
+// word, float32 one.
+template <bool BF16, bool VEC>
+struct Coords {
+  static constexpr int W = BF16 ? kE / 2 : kE;
+  uint32_t w[W];
 
-// LPB lanes (a power of two, at most 16) hold one block of 8 * LPB >= 128 or
+  __device__ __forceinline__ void load(const elem_t<BF16>* row, int c0, int D) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = 0;
+    if constexpr (VEC) {  // D % 8 == 0 and 16-byte rows
+      constexpr int V = BF16 ? 8 : 4;
+#pragma unroll
+      for (int i = 0; i < kE / V; ++i) {
+        if (c0 + i * V >= D) continue;
+        const uint4 u = __ldcs(reinterpret_cast<const uint4*>(row + c0 + i * V));
+        w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kE; ++i) {
+        if (c0 + i >= D) continue;
+        if constexpr (BF16) {
+          const uint32_t h = *reinterpret_cast<const uint16_t*>(row + c0 + i);
+          w[i / 2] |= i & 1 ? h << 16 : h;
+        } else {
+          w[i] = __float_as_uint(row[c0 + i]);
+        }
+      }
+    }
+  }
+  // Bits of the largest magnitude as a float32 (integer comparison: a NaN is
+  // the largest).
+  __device__ __forceinline__ uint32_t magnitude() const {
+    uint32_t a = 0;
+    if constexpr (BF16) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) a = max_u16x2(a, w[i] & 0x7fff7fffu);
+      return max(a << 16, a & 0xffff0000u);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) a = max(a, w[i] & 0x7fffffffu);
+      return a;
+    }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (BF16) return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    else return __uint_as_float(w[i]);
+  }
+};
+
+// LPB lanes (a power of two, at most 8) hold one block of 16 * LPB >= 128 or
 // >= D coordinates; rows * nb blocks in all.  I is the type block numbers fit
 // (a 64-bit division per block is slower than the block's arithmetic).
 template <bool BF16, bool VEC, int LPB, typename I>
 __global__ void __launch_bounds__(kQThreads) k_quantize(const elem_t<BF16>* __restrict__ X, I blocks, int nb, int D,
                                                         int64_t ld, uint8_t* __restrict__ q,
                                                         uint8_t* __restrict__ scale) {
+  constexpr int kU = BF16 ? 4 : 2;     // pieces in flight: 128 bytes a thread
   constexpr I kPer = kQThreads / LPB;  // blocks of one piece
   const int l = threadIdx.x % LPB;
   const I step = static_cast<I>(gridDim.x) * (kPer * kU);
   // every lane of a warp runs the same number of rounds: the shuffles below
   // take the whole warp
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * (kPer * kU); base < static_cast<int64_t>(blocks); base += step) {
-    float v[kU][kE];
-    int64_t row[kU];
+    Coords<BF16, VEC> v[kU];
+    I row[kU];
     int c0[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int64_t at = base + u * kPer + threadIdx.x / LPB;
       const bool on = at < static_cast<int64_t>(blocks);
-      const I blk = on ? static_cast<I>(at) : 0, r = nb == 1 ? blk : blk / static_cast<I>(nb);
-      row[u] = on ? static_cast<int64_t>(r) : -1;
-      c0[u] = static_cast<int>(blk - r * static_cast<I>(nb)) * kQBlock + l * kE;
-      load_coords<BF16, VEC>(X + static_cast<int64_t>(r) * D, on ? c0[u] : D, D, v[u]);
+      const I blk = on ? static_cast<I>(at) : 0;
+      row[u] = nb == 1 ? blk : blk / static_cast<I>(nb);
+      c0[u] = on ? static_cast<int>(blk - row[u] * static_cast<I>(nb)) * kQBlock + l * kE : D + kE;
+      v[u].load(X + static_cast<int64_t>(row[u]) * D, c0[u], D);
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      uint32_t a = 0;
-#pragma unroll
-      for (int i = 0; i < kE; ++i) a = max(a, __float_as_uint(v[u][i]) & 0x7fffffffu);
+      uint32_t a = v[u].magnitude();
 #pragma unroll
       for (int o = LPB / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
       // a = f * 2^k with f in [0.5, 1): a <= 448 * 2^e = 0.875 * 2^(e + 9) needs
@@ -102,18 +125,20 @@ __global__ void __launch_bounds__(kQThreads) k_quantize(const elem_t<BF16>* __re
       e = max(e, -117);
       const bool bad = a >= 0x7f800000u;  // an infinity or a NaN
       const float inv = bad ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      if (row[u] < 0) continue;
-      uint32_t w[2];
+      uint32_t w[kE / 4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[u][4 * h] * inv, v[u][4 * h + 1] * inv),
+      for (int h = 0; h < kE / 4; ++h) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[u].at(4 * h) * inv, v[u].at(4 * h + 1) * inv),
                                                      __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[u][4 * h + 2] * inv, v[u][4 * h + 3] * inv),
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[u].at(4 * h + 2) * inv, v[u].at(4 * h + 3) * inv),
                                                      __NV_SATFINITE, __NV_E4M3);
         w[h] = lo | (hi << 16);
       }
-      if (c0[u] < ld) *reinterpret_cast<uint2*>(q + row[u] * ld + c0[u]) = make_uint2(w[0], w[1]);
-      if (l == 0) scale[row[u] * nb + c0[u] / kQBlock] = bad ? 255 : static_cast<uint8_t>(e + 127);
+      // a lane at or behind the row's end has nothing to write (ld is a multiple of kE)
+      if (c0[u] < D)
+        *reinterpret_cast<uint4*>(q + static_cast<int64_t>(row[u]) * ld + c0[u]) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (l == 0 && c0[u] < D)
+        scale[static_cast<int64_t>(row[u]) * nb + c0[u] / kQBlock] = bad ? 255 : static_cast<uint8_t>(e + 127);
     }
   }
 }
@@ -123,8 +148,12 @@ __device__ __forceinline__ float e8m0(uint32_t b) {
   return __uint_as_float(b == 255u ? 0x7fc00000u : (b ? b << 23 : 0x00400000u));
 }
 
-constexpr int kDE = 16;  // coordinates per piece of k_dequantize: 16 bytes of q
-constexpr int kDU = 2;
+// Coordinates per piece of k_dequantize: 16 bytes of output, so that a warp's
+// store instruction writes whole sectors (two 16-byte stores to each 32 bytes
+// of a lane's own, taken apart, moved 2.5 times the sectors through L2).
+template <bool BF16>
+constexpr int kDE_of = BF16 ? 8 : 4;
+constexpr int kDU = 4;
 
 // gpr pieces per row.
 template <bool BF16, bool VEC, typename I>
@@ -132,10 +161,11 @@ __global__ void __launch_bounds__(kQThreads) k_dequantize(const uint8_t* __restr
                                                           const uint8_t* __restrict__ scale, I groups, int gpr, int nb,
                                                           int D, int64_t ld, int64_t ld_out,
                                                           elem_t<BF16>* __restrict__ X) {
+  constexpr int kDE = kDE_of<BF16>;
   const int64_t step = static_cast<int64_t>(gridDim.x) * (kQThreads * kDU);
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * (kQThreads * kDU) + threadIdx.x;
        base < static_cast<int64_t>(groups); base += step) {
-    uint4 u[kDU];
+    uint32_t u[kDU][kDE / 4];
     float s[kDU];
     int64_t row[kDU];
     int c0[kDU];
@@ -146,40 +176,39 @@ __global__ void __launch_bounds__(kQThreads) k_dequantize(const uint8_t* __restr
       const I g = on ? static_cast<I>(at) : 0, r = g / static_cast<I>(gpr);
       row[k] = on ? static_cast<int64_t>(r) : -1;
       c0[k] = static_cast<int>(g - r * static_cast<I>(gpr)) * kDE;
-      u[k] = __ldg(reinterpret_cast<const uint4*>(q + static_cast<int64_t>(r) * ld + c0[k]));
+      const uint8_t* src = q + static_cast<int64_t>(r) * ld + c0[k];
+      if constexpr (BF16) {
+        const uint2 w = __ldcs(reinterpret_cast<const uint2*>(src));
+        u[k][0] = w.x, u[k][1] = w.y;
+      } else {
+        u[k][0] = __ldcs(reinterpret_cast<const uint32_t*>(src));
+      }
       s[k] = e8m0(__ldg(scale + static_cast<int64_t>(r) * nb + c0[k] / kQBlock));
     }
 #pragma unroll
     for (int k = 0; k < kDU; ++k) {
       if (row[k] < 0) continue;
       float v[kDE];
-      const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
 #pragma unroll
       for (int i = 0; i < kDE / 2; ++i) {
         const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-            static_cast<__nv_fp8x2_storage_t>(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
+            static_cast<__nv_fp8x2_storage_t>(u[k][i / 2] >> (16 * (i & 1))), __NV_E4M3);
         const float2 f = __half22float2(__half2(h));
         v[2 * i] = f.x * s[k];
         v[2 * i + 1] = f.y * s[k];
       }
       elem_t<BF16>* out = X + row[k] * ld_out + c0[k];
-      if (VEC) {
+      if (VEC) {  // whole pieces: D is a multiple of 8
+        if constexpr (BF16) {
+          uint32_t o[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {  // 8 coordinates; D and the rows are multiples of 8
-          if (c0[k] + 8 * h >= D) break;
-          if constexpr (BF16) {
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[8 * h + 2 * i], v[8 * h + 2 * i + 1]);
-              o[i] = *reinterpret_cast<const uint32_t*>(&b2);
-            }
-            reinterpret_cast<uint4*>(out)[h] = make_uint4(o[0], o[1], o[2], o[3]);
-          } else {
-            reinterpret_cast<float4*>(out)[2 * h] = make_float4(v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3]);
-            reinterpret_cast<float4*>(out)[2 * h + 1] =
-                make_float4(v[8 * h + 4], v[8 * h + 5], v[8 * h + 6], v[8 * h + 7]);
+          for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            o[i] = *reinterpret_cast<const uint32_t*>(&b2);
           }
+          *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
+        } else {
+          *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
         }
       } else {
 #pragma unroll
@@ -201,7 +230,7 @@ unsigned grid_for(int64_t units, int64_t per_block) {
 
 template <bool BF16, bool VEC, int LPB>
 void quantize_t(const void* X, int64_t blocks, int nb, int D, uint8_t* q, uint8_t* scale, cudaStream_t s) {
-  const unsigned grid = grid_for(blocks, kQThreads / LPB * kU);
+  const unsigned grid = grid_for(blocks, kQThreads / LPB * (BF16 ? 4 : 2));
   const auto* x = static_cast<const elem_t<BF16>*>(X);
   if (blocks < (int64_t(1) << 31))
     k_quantize<BF16, VEC, LPB, uint32_t><<<grid, kQThreads, 0, s>>>(x, static_cast<uint32_t>(blocks), nb, D, q_ld(D), q, scale);
@@ -211,16 +240,16 @@ void quantize_t(const void* X, int64_t blocks, int nb, int D, uint8_t* q, uint8_
 
 template <bool BF16, bool VEC>
 void quantize_d(const void* X, int64_t blocks, int nb, int D, uint8_t* q, uint8_t* scale, cudaStream_t s) {
-  // lanes per block: 16 cover 128 coordinates; narrower points need fewer
-  if (D > 64) quantize_t<BF16, VEC, 16>(X, blocks, nb, D, q, scale, s);
-  else if (D > 32) quantize_t<BF16, VEC, 8>(X, blocks, nb, D, q, scale, s);
-  else if (D > 16) quantize_t<BF16, VEC, 4>(X, blocks, nb, D, q, scale, s);
-  else quantize_t<BF16, VEC, 2>(X, blocks, nb, D, q, scale, s);
+  // lanes per block: 8 cover 128 coordinates; narrower points need fewer
+  if (D > 64) quantize_t<BF16, VEC, 8>(X, blocks, nb, D, q, scale, s);
+  else if (D > 32) quantize_t<BF16, VEC, 4>(X, blocks, nb, D, q, scale, s);
+  else if (D > 16) quantize_t<BF16, VEC, 2>(X, blocks, nb, D, q, scale, s);
+  else quantize_t<BF16, VEC, 1>(X, blocks, nb, D, q, scale, s);
 }
 
 template <bool BF16, bool VEC>
 void dequantize_t(const uint8_t* q, const uint8_t* scale, int64_t rows, int D, int64_t ld_out, void* X, cudaStream_t s) {
-  const int gpr = (D + kDE - 1) / kDE;
+  const int gpr = (D + kDE_of<BF16> - 1) / kDE_of<BF16>;
   const int64_t groups = rows * gpr;
   const unsigned grid = grid_for(groups, kQThreads * kDU);
   auto* o = static_cast<elem_t<BF16>*>(X);

@@ -41,7 +41,7 @@ constexpr int kBM = 128, kBN = 128;
 constexpr int kOpBytes = kBM * kQBlock;  // 16 KB: 128 rows of one block
 constexpr uint32_t kTmemCols = 512;      // the accumulators and the scales (powers of two only)
 constexpr uint32_t kSfBase = kAccs * kBN;
-constexpr int kEpiBytes = kStageBytes + kBN * 4;  // a warp's staging rows and its copy of the tile's bias
+constexpr int kEpiBytes = kStageBytes + kBN * 4;  // per warp: staging rows, and (behind all of those) the tile's bias
 // k_scores_wide: stages of one block of each operand, stages of scales
 constexpr int kStages = 5;
 constexpr int kStageOps = 2 * kOpBytes;
@@ -68,7 +68,8 @@ struct ScoresK {
   int run;         // k_scores_near: centroid tiles held together
   int64_t runs, units;  // runs per instance, (instance, run, point tile) triples
   void* S;
-  bool vec;
+  bool boxes;  // S goes out as boxes of its tensor map (rows of 16 bytes), else word by word
+  bool pairs;  // bf16 without boxes: rows of 4 bytes
   unsigned int* status;
   uint64_t limit_ns;
 };
@@ -135,19 +136,15 @@ __device__ __forceinline__ float4 load_bias(const ScoresK& p, int b, int n0, int
 }
 
 // One accumulator to S: 32 points per warp, the tile's 128 columns in staged
-// lines of 128 bytes; the TMEM loads run one 32-column chunk ahead.  buf is
-// the warp's staging rows and, behind them, its bias.
+// lines of 128 bytes; the TMEM loads run one 32-column chunk ahead.
 template <bool BF16>
-__device__ __forceinline__ void emit_tile(const ScoresK& p, int b, int64_t m, int n0, uint32_t tm, uint64_t* empty,
-                                          uint8_t* buf, float4 bias4, int lane) {
+__device__ __forceinline__ void emit_tile(const ScoresK& p, const CUtensorMap* smap, int b, int64_t m, int n0, uint32_t tm,
+                                          uint64_t* empty, uint8_t* stage, float* bias, float4 bias4, int lane) {
   constexpr int ES = BF16 ? 2 : 4;
   constexpr int kCols = 128 / ES;  // columns of a staged line
   const int rows = static_cast<int>(m + 32 <= p.N ? 32 : (p.N > m ? p.N - m : 0));
   const int64_t row_bytes = static_cast<int64_t>(p.K) * ES;
-  uint8_t* out = static_cast<uint8_t*>(p.S) + (static_cast<int64_t>(b) * p.N + m) * row_bytes +
-                 static_cast<int64_t>(n0) * ES;
   const int ncol = p.K - n0 < kBN ? p.K - n0 : kBN;
-  float* bias = reinterpret_cast<float*>(buf + kStageBytes);
   reinterpret_cast<float4*>(bias)[lane] = bias4;
   __syncwarp();
   uint32_t r[2][32];
@@ -166,13 +163,21 @@ __device__ __forceinline__ void emit_tile(const ScoresK& p, int b, int64_t m, in
       v[4 * i + 3] = fmaf(__uint_as_float(r[c & 1][4 * i + 3]), p.alpha, bv.w);
     }
     const int c0 = BF16 ? (c & ~1) * 32 : c * 32;  // first column of the staged line
-    if constexpr (BF16) stage_bf16(buf, v, c & 1, lane);
-    else stage_f32(buf, v, lane);
-    if (!BF16 || (c & 1)) {
-      __syncwarp();
-      const int n = ncol - c0 < kCols ? ncol - c0 : kCols;
-      if (n > 0) store_staged<ES>(buf, out + c0 * ES, row_bytes, rows, n * ES, p.vec, lane);
-      __syncwarp();
+    if (p.boxes && (!BF16 || !(c & 1))) stage_reusable(lane);
+    if constexpr (BF16) stage_bf16(stage, v, c & 1, lane);
+    else stage_f32(stage, v, lane);
+    if ((!BF16 || (c & 1)) && c0 < ncol) {
+      if (p.boxes) {
+        if (rows > 0) store_box(stage, smap, n0 + c0, static_cast<int>(m), b, lane);
+      } else {
+        __syncwarp();
+        const int n = ncol - c0 < kCols ? ncol - c0 : kCols;
+        uint8_t* out = static_cast<uint8_t*>(p.S) + (static_cast<int64_t>(b) * p.N + m) * row_bytes +
+                       static_cast<int64_t>(n0 + c0) * ES;
+        if (!BF16 || p.pairs) store_words<4>(stage, out, row_bytes, rows, n * ES / 4, lane);
+        else store_words<2>(stage, out, row_bytes, rows, n, lane);
+        __syncwarp();
+      }
     }
     if (c + 1 < kBN / 32) {
       tmem_wait32(r[(c + 1) & 1]);
@@ -304,7 +309,8 @@ struct UnitPos {
 
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_scores_near(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap cmap, const ScoresK p) {
+    k_scores_near(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap cmap,
+             const __grid_constant__ CUtensorMap smap, const ScoresK p) {
   extern __shared__ uint8_t smem_raw[];
   const Setup su = scores_setup(smem_raw);
   Bars& bars = *su.bars;
@@ -409,7 +415,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 8) {
     const int q4 = warp & 3, grp = (warp - 8) >> 2;
     const uint32_t tm = su.tmem + (static_cast<uint32_t>(q4 * 32) << 16) + static_cast<uint32_t>(grp * kBN);
-    uint8_t* buf = su.epi + (warp - 8) * kEpiBytes;
+    uint8_t* stage = su.epi + (warp - 8) * kStageBytes;
+    float* bias = reinterpret_cast<float*>(su.epi + kEpiWarps * kStageBytes) + (warp - 8) * kBN;
     uint32_t aph = 0;
     int ab = 0;
     bool ok = true;
@@ -425,16 +432,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!__all_sync(0xffffffffu, mbar_wait(&bars.a_full[grp], aph, g))) { ok = false; break; }
         aph ^= 1u;
         tc_fence_after();
-        emit_tile<BF16>(p, q.b, q.m * kBM + q4 * 32, n0, tm, &bars.a_empty[grp], buf, bias4, lane);
+        emit_tile<BF16>(p, &smap, q.b, q.m * kBM + q4 * 32, n0, tm, &bars.a_empty[grp], stage, bias, bias4, lane);
       }
     }
+    stage_reusable(lane);
   }
   scores_teardown(su);
 }
 
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_scores_wide(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap cmap, const ScoresK p) {
+    k_scores_wide(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap cmap,
+             const __grid_constant__ CUtensorMap smap, const ScoresK p) {
   extern __shared__ uint8_t smem_raw[];
   const Setup su = scores_setup(smem_raw);
   Bars& bars = *su.bars;
@@ -515,7 +524,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 8) {
     const int q4 = warp & 3, grp = (warp - 8) >> 2;
     const uint32_t tm = su.tmem + (static_cast<uint32_t>(q4 * 32) << 16) + static_cast<uint32_t>(grp * kBN);
-    uint8_t* buf = su.epi + (warp - 8) * kEpiBytes;
+    uint8_t* stage = su.epi + (warp - 8) * kStageBytes;
+    float* bias = reinterpret_cast<float*>(su.epi + kEpiWarps * kStageBytes) + (warp - 8) * kBN;
     uint32_t aph = 0;
     int ab = 0;
     for (int64_t t = blockIdx.x; t < p.ntiles; t += gridDim.x) {
@@ -527,8 +537,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!__all_sync(0xffffffffu, mbar_wait(&bars.a_full[grp], aph, g))) break;
       aph ^= 1u;
       tc_fence_after();
-      emit_tile<BF16>(p, tp.b, tp.m0 + q4 * 32, tp.n0, tm, &bars.a_empty[grp], buf, bias4, lane);
+      emit_tile<BF16>(p, &smap, tp.b, tp.m0 + q4 * 32, tp.n0, tm, &bars.a_empty[grp], stage, bias, bias4, lane);
     }
+    stage_reusable(lane);
   }
   scores_teardown(su);
 }
@@ -552,7 +563,8 @@ cudaError_t launch_scores(const ScoresArgs& a, cudaStream_t s) {
   k.ntiles = k.mt * k.nt * a.B;
   k.S = a.S;
   const int es = a.dtype == kDtypeBF16 ? 2 : 4;
-  k.vec = static_cast<int64_t>(a.K) * es % 16 == 0 && reinterpret_cast<uintptr_t>(a.S) % 16 == 0;
+  k.boxes = a.smap != nullptr;
+  k.pairs = es == 2 && a.K % 2 == 0 && reinterpret_cast<uintptr_t>(a.S) % 4 == 0;
   k.status = a.status;
   k.limit_ns = a.limit_ns;
   int dev = 0, nsm = 0;
@@ -579,7 +591,7 @@ cudaError_t launch_scores(const ScoresArgs& a, cudaStream_t s) {
   chain_break();
   if (fault_hit(kFaultLaunch)) return cudaErrorLaunchFailure;
   count_launch();
-  kern<<<static_cast<unsigned>(grid < nsm ? grid : nsm), kThreads, kSmem, s>>>(*a.xmap, *a.cmap, k);
+  kern<<<static_cast<unsigned>(grid < nsm ? grid : nsm), kThreads, kSmem, s>>>(*a.xmap, *a.cmap, a.smap ? *a.smap : *a.cmap, k);
   return cudaGetLastError();
 }
 

@@ -190,10 +190,15 @@ int km_scores(const uint8_t* xq, const uint8_t* xs, const uint8_t* cq, const uin
   if (r != KM_OK) return r;
   SOFT_CUDA(cudaMemsetAsync(c.status(), 0, sizeof(unsigned int), c.s));
   if (N == 0) return KM_OK;
-  CUtensorMap xmap, cmap;
+  CUtensorMap xmap, cmap, smap;
   if ((r = encode_q(&xmap, xq, D, N, B)) != KM_OK) return r;
   if ((r = encode_q(&cmap, cq, D, K, B)) != KM_OK) return r;
-  const ScoresArgs a{&xmap, &cmap, xs, cs, bias, alpha, B, N, D, K, dtype, S, c.status(), api_wait_limit_ns()};
+  const bool f32 = dtype == KM_F32;
+  const bool boxes = K % (f32 ? 4 : 8) == 0 && aligned16(S);
+  if (boxes && (r = encode(&smap, S, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                           f32 ? 4 : 2, K, K, N, B, 32)) != KM_OK)
+    return r;
+  const ScoresArgs a{&xmap, &cmap, boxes ? &smap : nullptr, xs, cs, bias, alpha, B, N, D, K, dtype, S, c.status(), api_wait_limit_ns()};
   SOFT_CUDA(launch_scores(a, c.s));
   return KM_OK;
 }

@@ -41,6 +41,7 @@ cudaError_t launch_dequantize(const uint8_t* q, const uint8_t* scale, int dtype,
 struct ScoresArgs {
   const CUtensorMap* xmap;  // [B][N][D] e4m3, box 128 coordinates x 128 points
   const CUtensorMap* cmap;  // [B][K][D] e4m3, box 128 coordinates x 128 centroids
+  const CUtensorMap* smap;  // [B][N][K] dtype, box 128 bytes x 32 points; null where S's rows are not of 16 bytes
   const uint8_t* xs;
   const uint8_t* cs;
   const float* bias;  // [B][K] or null

@@ -4,6 +4,8 @@
 
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "km_ptx.cuh"
 
 namespace km {
@@ -35,58 +37,70 @@ __device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
                : "memory");
 }
 
-// Output staging of one epilogue warp: 32 rows of 128 bytes, 16 bytes of
-// padding per row so that the row-per-lane writes and the line-per-row reads
-// both run without bank conflicts.
-constexpr int kStageRow = 144;
-constexpr int kStageBytes = 32 * kStageRow;
-
-// 128 bytes of each of the warp's 32 rows (staged, lane = row on the way in)
-// to global rows dst + r * row_bytes: `rows` rows are in range, `bytes` of the
-// 128 are, and both the rows and dst start on 16-byte boundaries when vec.
-// ES is the element size.
-template <int ES>
-__device__ __forceinline__ void store_staged(const uint8_t* stage, uint8_t* dst, int64_t row_bytes, int rows, int bytes,
-                                             bool vec, int lane) {
-  if (vec && bytes == 128) {
-    const int c = (lane & 7) * 16;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = i * 4 + (lane >> 3);
-      if (r < rows) {
-        const uint4 v = *reinterpret_cast<const uint4*>(stage + r * kStageRow + c);
-        *reinterpret_cast<uint4*>(dst + r * row_bytes + c) = v;
-      }
-    }
-    return;
-  }
-  // ragged edge or unaligned rows: one element per lane, a row at a time
-  using E = typename std::conditional<ES == 2, uint16_t, uint32_t>::type;
-  const int n = bytes / ES;
-  for (int r = 0; r < rows; ++r)
-    for (int c = lane; c < n; c += 32)
-      reinterpret_cast<E*>(dst + r * row_bytes)[c] = reinterpret_cast<const E*>(stage + r * kStageRow)[c];
-}
-
-// This lane's row of 32 float32 columns into its staging row: all 128 bytes
-// (float32), or half `half` of them (bf16, rounded to nearest even).
-__device__ __forceinline__ void stage_f32(uint8_t* stage, const float (&v)[32], int lane) {
-  float4* p = reinterpret_cast<float4*>(stage + lane * kStageRow);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) p[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-}
+// Output staging of one epilogue warp: 32 rows of 128 bytes, the 16-byte piece
+// c of row r at place c ^ (r % 8) (the tensor maps' 128-byte swizzle), so that
+// the row-per-lane writes and the line-per-row reads both run without bank
+// conflicts.  1024-byte aligned.
+constexpr int kStageBytes = 32 * 128;
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// This lane's row of 32 float32 columns into its staging row: all 128 bytes
+// (float32), or half `half` of them (bf16, rounded to nearest even).
+__device__ __forceinline__ void stage_f32(uint8_t* stage, const float (&v)[32], int lane) {
+  uint8_t* row = stage + lane * 128;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<float4*>(row + ((i ^ (lane & 7)) << 4)) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+}
+
 __device__ __forceinline__ void stage_bf16(uint8_t* stage, const float (&v)[32], int half, int lane) {
-  uint4* p = reinterpret_cast<uint4*>(stage + lane * kStageRow + half * 64);
+  uint8_t* row = stage + lane * 128;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    p[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                      pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+    *reinterpret_cast<uint4*>(row + (((half * 4 + i) ^ (lane & 7)) << 4)) =
+        make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                   pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+}
+
+// The warp's staged 32 x 128-byte box to (x, y, z) of a tensor map with that
+// box (rows and columns out of range are not written).  stage_reusable waits
+// until such a store has read the staging rows.
+__device__ __forceinline__ void store_box(const uint8_t* stage, const CUtensorMap* map, int x, int y, int z, int lane) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(smem_addr(stage))
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
+__device__ __forceinline__ void stage_reusable(int lane) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
+}
+
+// The staged rows to rows of any alignment, words of W bytes (4 or 2) one per
+// lane, a row at a time: `rows` rows and `words` words of each are in range.
+template <int W>
+__device__ __forceinline__ void store_words(const uint8_t* stage, uint8_t* dst, int64_t row_bytes, int rows, int words,
+                                            int lane) {
+  using E = typename std::conditional<W == 2, uint16_t, uint32_t>::type;
+#pragma unroll
+  for (int h = 0; h < 4 / W; ++h) {
+    const int o = (h * 32 + lane) * W;
+    const bool in = h * 32 + lane < words;
+#pragma unroll 16
+    for (int r = 0; r < 32; ++r)
+      if (in && r < rows)
+        *reinterpret_cast<E*>(dst + r * row_bytes + o) =
+            *reinterpret_cast<const E*>(stage + r * 128 + (((o >> 4) ^ (r & 7)) << 4) + (o & 15));
+  }
 }
 
 }  // namespace km
