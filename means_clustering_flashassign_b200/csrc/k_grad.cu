@@ -90,6 +90,13 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
   return d;
 }
 
+// s0 += the low half of w, s1 += the high one (bf16, added in float32).
+__device__ __forceinline__ void add_bf16x2(float& s0, float& s1, uint32_t w) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.f32.bf16 %0, l, %0;\n\tadd.f32.bf16 %1, h, %1;\n\t}"
+      : "+f"(s0), "+f"(s1)
+      : "r"(w));
+}
+
 // KT centroids per dC tile (the MMA's N).
 template <int KT, bool OUT_BF16, bool WX, bool WC, bool WB>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -329,9 +336,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (WB) {
-    // column sums: each warp sums its share of a slice's points for 64 centroids, two per lane
+    // column sums: each warp takes its share of a slice's points for 64
+    // centroids; a lane has 8 centroids (16 bytes) of every fourth of them
     constexpr int kParts = kSumWarps / (KT / 64);  // warps that share 64 centroids
     constexpr int kN = kSlice / kParts;            // points of a slice per warp
+    constexpr int kFlush = 64 / kN;                // slices until a lane has summed 16 points
     const int cw = warp - 2 - kEpiWarps, box = cw / kParts, part = cw % kParts;
     int st = 0;
     uint32_t ph = 0;
@@ -341,7 +350,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Walk w(item, p);
       for (int ps = 0; ok && ps < p.passes; ++ps) {
         const int kt = ps * p.group + me;
-        double a0 = 0.0, a1 = 0.0;
+        double sum[8] = {};
+        float s[8] = {};
+        int held = 0;
+        auto flush = [&]() {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sum[j] += s[j], s[j] = 0.f;
+          held = 0;
+        };
         for (int64_t t = w.t0; ok && t < w.t1; t += p.group) {
           const int nx = WX && ps == 0 && t + me < w.t1 ? kslices * p.planes : 0;
           for (int i = 0; i < nx; ++i) {  // dX's slices: not looked at
@@ -357,19 +373,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint8_t* bx = ops + st * kStageB + kABytes + box * kBoxBytes;
               if (w.dt == 0) {
 #pragma unroll
-                for (int h = 0; h < kN; h += 16) {
-                  float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-                  for (int j = 0; j < (kN < 16 ? kN : 16); ++j) {
-                    const int r = part * kN + h + j;
-                    const uint32_t v = *reinterpret_cast<const uint32_t*>(
-                        bx + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2)));
-                    s0 += __uint_as_float(v << 16);
-                    s1 += __uint_as_float(v & 0xffff0000u);
-                  }
-                  a0 += s0;
-                  a1 += s1;
+                for (int h = 0; h < kN; h += 4) {
+                  const int r = part * kN + h + (lane >> 3);
+                  const uint4 v = *reinterpret_cast<const uint4*>(bx + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+                  add_bf16x2(s[0], s[1], v.x);
+                  add_bf16x2(s[2], s[3], v.y);
+                  add_bf16x2(s[4], s[5], v.z);
+                  add_bf16x2(s[6], s[7], v.w);
                 }
+                if (++held == kFlush) flush();
               }
               __syncwarp();
               if (lane == 0) mbar_arrive(&empty[st]);
@@ -379,10 +391,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         if (w.dt == 0 && kt < p.nkt) {
-          const int k = kt * KT + box * 64 + lane * 2;
+          flush();
           float* o = p.db + (static_cast<int64_t>(w.split * kParts + part) * p.B + w.b) * p.K;
-          if (k < p.K) o[k] = static_cast<float>(a0);
-          if (k + 1 < p.K) o[k + 1] = static_cast<float>(a1);
+          const int k = kt * KT + box * 64 + lane * 8;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 8);
+            sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 16);
+            if (lane < 8 && k + j < p.K) o[k + j] = static_cast<float>(sum[j]);
+          }
         }
       }
     }

@@ -42,18 +42,22 @@ constexpr int kOpBytes = kBM * kQBlock;  // 16 KB: 128 rows of one block
 constexpr uint32_t kTmemCols = 512;      // the accumulators and the scales (powers of two only)
 constexpr uint32_t kSfBase = kAccs * kBN;
 constexpr int kEpiBytes = kStageBytes + kBN * 4;  // per warp: staging rows, and (behind all of those) the tile's bias
-// k_scores_wide: stages of one block of each operand, stages of scales
-constexpr int kStages = 5;
-constexpr int kStageOps = 2 * kOpBytes;
+constexpr int kBarBytes = 320;
+// k_scores_wide: a CTA takes a point tile against two centroid tiles at once
+// (three 16 KB blocks per 128 coordinates instead of four: L2's bandwidth to
+// the SMs bounds it); stages of one block of each, stages of scales
+constexpr int kWideRun = 2;
+constexpr int kStages = 3;
+constexpr int kStageOps = (1 + kWideRun) * kOpBytes;
 constexpr int kSfStages = 8;
-constexpr int kSfCols = 8;               // 4 TMEM columns of scales per operand
+constexpr int kSfCols = 4 * (1 + kWideRun);  // 4 TMEM columns of scales per tile
 // k_scores_near: operand tiles in all; point tiles and their scales are double
 // and four times buffered, the rest holds centroid tiles
 constexpr int kNearTiles = 10;
 constexpr int kNearSfA = 4;
 constexpr int kNearMaxRun = 8;           // centroid tiles held (and 4 TMEM columns of scales for each)
-constexpr size_t kSmem = 1024 + kNearTiles * kOpBytes + kEpiWarps * kEpiBytes + 64 * 8;
-static_assert(kNearTiles * kOpBytes == kStages * kStageOps, "one shared-memory layout for both kernels");
+constexpr size_t kSmem = 1024 + kNearTiles * kOpBytes + kEpiWarps * kEpiBytes + kBarBytes;
+static_assert(kNearTiles * kOpBytes >= kStages * kStageOps && kWideRun <= kAccs, "one shared-memory layout for both kernels");
 static_assert(kSfBase + kSfStages * kSfCols <= kTmemCols && kSfBase + 4 * (kNearMaxRun + kNearSfA) <= kTmemCols, "TMEM");
 
 struct ScoresK {
@@ -64,25 +68,28 @@ struct ScoresK {
   int B, K, nb, D;
   int64_t N;
   int64_t mt, nt;  // tiles per instance
-  int64_t ntiles;  // k_scores_wide
-  int run;         // k_scores_near: centroid tiles held together
-  int64_t runs, units;  // runs per instance, (instance, run, point tile) triples
+  int64_t ntiles;
+  int64_t runs;    // runs of centroid tiles per instance
+  int64_t units;   // k_scores_wide: (instance, point tile, run) triples
   void* S;
-  bool boxes;  // S goes out as boxes of its tensor map (rows of 16 bytes), else word by word
-  bool pairs;  // bf16 without boxes: rows of 4 bytes
+  bool boxes;  // S goes out as boxes of its tensor map (rows of 16 bytes)
+  bool pairs;  // else, bf16: two at a time (rows of 4 bytes)
   unsigned int* status;
   uint64_t limit_ns;
 };
 
+// k_scores_wide: a point tile and n centroid tiles from n0 on.
 struct TilePos {
-  int b;
+  int b, n;
   int64_t m0;
   int n0;
 };
 __device__ __forceinline__ TilePos tile_pos(int64_t t, const ScoresK& p) {
-  const int64_t n = t % p.nt, r = t / p.nt;
+  const int64_t n = t % p.runs, r = t / p.runs;
   const int64_t b = r / p.mt;
-  return {static_cast<int>(b), (r - b * p.mt) * kBM, static_cast<int>(n * kBN)};
+  const int64_t left = p.nt - n * kWideRun;
+  return {static_cast<int>(b), static_cast<int>(left < kWideRun ? left : kWideRun), (r - b * p.mt) * kBM,
+          static_cast<int>(n * kWideRun * kBN)};
 }
 
 // Block-scaled MMA, M = N = 128, e4m3 operands (both K-major), e8m0 scales:
@@ -174,8 +181,9 @@ __device__ __forceinline__ void emit_tile(const ScoresK& p, const CUtensorMap* s
         const int n = ncol - c0 < kCols ? ncol - c0 : kCols;
         uint8_t* out = static_cast<uint8_t*>(p.S) + (static_cast<int64_t>(b) * p.N + m) * row_bytes +
                        static_cast<int64_t>(n0 + c0) * ES;
-        if (!BF16 || p.pairs) store_words<4>(stage, out, row_bytes, rows, n * ES / 4, lane);
-        else store_words<2>(stage, out, row_bytes, rows, n, lane);
+        if (n < kCols || rows < 32) store_ragged<ES>(stage, out, row_bytes, rows, n, lane);
+        else if (!BF16 || p.pairs) store_lines<4>(stage, out, static_cast<uint32_t>(row_bytes), lane);
+        else store_lines<2>(stage, out, static_cast<uint32_t>(row_bytes), lane);
         __syncwarp();
       }
     }
@@ -201,7 +209,7 @@ struct Bars {
   uint32_t tmem;
   int abort_flag;
 };
-static_assert(sizeof(Bars) <= 64 * 8, "barrier space");
+static_assert(sizeof(Bars) <= kBarBytes && kSmem <= 232448, "shared memory");
 
 struct Setup {
   uint8_t* ops;
@@ -284,27 +292,37 @@ __device__ __forceinline__ void block_mma(uint32_t d, uint32_t a, uint32_t b, in
 
 // Narrow points: units (instance, run of centroid tiles, point tile), point
 // tiles fastest; a CTA takes consecutive units and reloads the centroids only
-// where the run changes.
+// where the run changes.  Run r of an instance holds its centroid tiles
+// [r nt / runs, (r + 1) nt / runs), and the CTAs' shares are cut by tiles, so
+// that runs of different lengths leave no CTA with more work.
 struct UnitPos {
-  int b, r;
+  int b, r, j0, j1;  // instance, run, its centroid tiles
   int64_t m;
-  __device__ __forceinline__ UnitPos(int64_t u, const ScoresK& p) {
-    const int64_t q = u / p.mt;
-    m = u - q * p.mt;
-    b = static_cast<int>(q / p.runs);
-    r = static_cast<int>(q - static_cast<int64_t>(b) * p.runs);
+  __device__ __forceinline__ void set_run(const ScoresK& p) {
+    j0 = static_cast<int>(r * p.nt / p.runs);
+    j1 = static_cast<int>((r + 1) * p.nt / p.runs);
+  }
+  // the first unit at or behind tile t (units of one run hold j1 - j0 tiles each)
+  __device__ __forceinline__ UnitPos(int64_t t, const ScoresK& p) {
+    const int64_t per = p.mt * p.nt;
+    b = static_cast<int>(t / per);
+    const int64_t in = t - b * per;
+    r = static_cast<int>(((in / p.mt + 1) * p.runs - 1) / p.nt);  // the run that holds tile in / mt
+    set_run(p);
+    m = (in - j0 * p.mt + (j1 - j0) - 1) / (j1 - j0);
+    if (m == p.mt) {
+      --m;
+      next(p);
+    }
   }
   __device__ __forceinline__ void next(const ScoresK& p) {
     if (++m == p.mt) {
       m = 0;
       if (++r == p.runs) { r = 0; ++b; }
+      set_run(p);
     }
   }
-  // centroid tiles of this run
-  __device__ __forceinline__ int tiles(const ScoresK& p) const {
-    const int64_t n = p.nt - static_cast<int64_t>(r) * p.run;
-    return n < p.run ? static_cast<int>(n) : p.run;
-  }
+  __device__ __forceinline__ bool operator!=(const UnitPos& o) const { return m != o.m || r != o.r || b != o.b; }
 };
 
 template <bool BF16>
@@ -318,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nb = p.nb;
   uint8_t* cops = su.ops + 2 * nb * kOpBytes;  // the centroid run, behind two point tiles
-  const int64_t u0 = blockIdx.x * p.units / gridDim.x, u1 = (blockIdx.x + 1) * p.units / gridDim.x;
+  const UnitPos first(blockIdx.x * p.ntiles / gridDim.x, p), end((blockIdx.x + 1) * p.ntiles / gridDim.x, p);
   const uint32_t sfb = su.tmem + kSfBase, sfa = sfb + 4 * kNearMaxRun;
 
   if (warp == 0) {
@@ -327,15 +345,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       prefetch_tensormap(&cmap);
       int st = 0, issued[2] = {-1, -1}, b_issued = -1;
       uint32_t ph = 0, bph = 0;
-      UnitPos q(u0, p);
-      for (int64_t u = u0; u < u1; ++u, q.next(p)) {
-        if (u == u0 || q.m == 0) {
+      bool fresh = true;
+      for (UnitPos q = first; q != end; q.next(p)) {
+        if (fresh || q.m == 0) {
+          fresh = false;
           if (!mbar_wait(&bars.b_empty, bph ^ 1u, g)) break;
-          const int n = q.tiles(p);
+          const int n = q.j1 - q.j0;
           mbar_arrive_expect_tx(&bars.b_full, static_cast<uint32_t>(n * nb * kOpBytes));
           for (int j = 0; j < n; ++j)
             for (int kb = 0; kb < nb; ++kb)
-              tma_load_3d(cops + (j * nb + kb) * kOpBytes, &cmap, kb * kQBlock, (q.r * p.run + j) * kBN, q.b, &bars.b_full);
+              tma_load_3d(cops + (j * nb + kb) * kOpBytes, &cmap, kb * kQBlock, (q.j0 + j) * kBN, q.b, &bars.b_full);
           b_issued = static_cast<int>(bph);
           bph ^= 1u;
         }
@@ -359,14 +378,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       int st = 0, ss = 0, ab = 0;
       uint32_t ph = 0, sph = 0, aph = 0, bph = 0;
       bool ok = true;
-      UnitPos q(u0, p);
-      for (int64_t u = u0; ok && u < u1; ++u) {
-        if (u == u0 || q.m == 0) {
+      bool fresh = true;
+      UnitPos q = first;
+      while (ok && q != end) {
+        if (fresh || q.m == 0) {
+          fresh = false;
           if (!mbar_wait(&bars.b_full, bph, g) || !mbar_wait(&bars.sfb_full, bph, g)) break;
           bph ^= 1u;
         }
         if (!mbar_wait(&bars.sf_full[ss], sph, g) || !mbar_wait(&bars.full[st], ph, g)) break;
-        const int n = q.tiles(p);
+        const int n = q.j1 - q.j0;
         const uint32_t a = smem_addr(su.ops + st * nb * kOpBytes), c = smem_addr(cops);
         for (int j = 0; j < n; ++j) {
           if (!mbar_wait(&bars.a_empty[ab], aph ^ 1u, g)) { ok = false; break; }
@@ -393,16 +414,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     int ss = 0;
     uint32_t sph = 0, bph = 0;
-    UnitPos q(u0, p);
-    for (int64_t u = u0; u < u1; ++u, q.next(p)) {
-      if (u == u0 || q.m == 0) {
+    bool fresh = true;
+    for (UnitPos q = first; q != end; q.next(p)) {
+      if (fresh || q.m == 0) {
+        fresh = false;
         if (!__all_sync(0xffffffffu, mbar_wait(&bars.b_empty, bph ^ 1u, g))) break;
         bph ^= 1u;
         tc_fence_after();
-        const int n = q.tiles(p);
-        for (int j = 0; j < n; ++j)
+        for (int j = 0; j < q.j1 - q.j0; ++j)
           store_scales(sfb + lane_off + static_cast<uint32_t>(4 * j), p.cs + static_cast<int64_t>(q.b) * p.K * nb,
-                       static_cast<int64_t>(q.r * p.run + j) * kBN, p.K, nb, 0, lane);
+                       static_cast<int64_t>(q.j0 + j) * kBN, p.K, nb, 0, lane);
         publish_scales(&bars.sfb_full, lane);
       }
       if (!__all_sync(0xffffffffu, mbar_wait(&bars.sf_empty[ss], sph ^ 1u, g))) break;
@@ -420,14 +441,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t aph = 0;
     int ab = 0;
     bool ok = true;
-    UnitPos q(u0, p);
-    for (int64_t u = u0; ok && u < u1; ++u, q.next(p)) {
-      const int n = q.tiles(p);
-      for (int j = 0; j < n; ++j) {
+    for (UnitPos q = first; ok && q != end; q.next(p)) {
+      for (int j = q.j0; j < q.j1; ++j) {
         const bool mine = ab == grp;
         if (++ab == kAccs) ab = 0;
         if (!mine) continue;
-        const int n0 = (q.r * p.run + j) * kBN;
+        const int n0 = j * kBN;
         const float4 bias4 = load_bias(p, q.b, n0, lane);
         if (!__all_sync(0xffffffffu, mbar_wait(&bars.a_full[grp], aph, g))) { ok = false; break; }
         aph ^= 1u;
@@ -461,14 +480,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < kStages; ++i) issued[i] = -1;
       bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < p.ntiles; t += gridDim.x) {
+      for (int64_t t = blockIdx.x; ok && t < p.units; t += gridDim.x) {
         const TilePos tp = tile_pos(t, p);
         for (int kb = 0; kb < nb; ++kb) {
           if (!mbar_wait(&bars.empty[st], ph ^ 1u, g)) { ok = false; break; }
           uint8_t* dst = su.ops + st * kStageOps;
-          mbar_arrive_expect_tx(&bars.full[st], kStageOps);
+          mbar_arrive_expect_tx(&bars.full[st], static_cast<uint32_t>((1 + tp.n) * kOpBytes));
           tma_load_3d(dst, &xmap, kb * kQBlock, static_cast<int>(tp.m0), tp.b, &bars.full[st]);
-          tma_load_3d(dst + kOpBytes, &cmap, kb * kQBlock, tp.n0, tp.b, &bars.full[st]);
+          for (int j = 0; j < tp.n; ++j)
+            tma_load_3d(dst + (1 + j) * kOpBytes, &cmap, kb * kQBlock, tp.n0 + j * kBN, tp.b, &bars.full[st]);
           issued[st] = static_cast<int>(ph);
           if (++st == kStages) { st = 0; ph ^= 1u; }
         }
@@ -481,15 +501,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       int st = 0, ss = 0, ab = 0;
       uint32_t ph = 0, sph = 0, aph = 0;
       bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < p.ntiles; t += gridDim.x) {
-        if (!mbar_wait(&bars.a_empty[ab], aph ^ 1u, g)) break;
+      for (int64_t t = blockIdx.x; ok && t < p.units; t += gridDim.x) {
+        const int n = tile_pos(t, p).n;
+        uint32_t acc[kWideRun];
+        int at[kWideRun];
+#pragma unroll
+        for (int j = 0; j < kWideRun; ++j) {
+          if (j >= n) break;
+          if (!mbar_wait(&bars.a_empty[ab], aph ^ 1u, g)) { ok = false; break; }
+          acc[j] = su.tmem + static_cast<uint32_t>(ab * kBN);
+          at[j] = ab;
+          if (++ab == kAccs) { ab = 0; aph ^= 1u; }
+        }
+        if (!ok) break;
         for (int kb = 0; kb < nb; ++kb) {
           if ((kb & 3) == 0 && !mbar_wait(&bars.sf_full[ss], sph, g)) { ok = false; break; }
           if (!mbar_wait(&bars.full[st], ph, g)) { ok = false; break; }
           tc_fence_after();
           const uint32_t a = smem_addr(su.ops + st * kStageOps);
           const uint32_t sf = su.tmem + kSfBase + static_cast<uint32_t>(ss * kSfCols);
-          block_mma(su.tmem + static_cast<uint32_t>(ab * kBN), a, a + kOpBytes, kb, p.D, sf, sf + 4);
+#pragma unroll
+          for (int j = 0; j < kWideRun; ++j)
+            if (j < n) block_mma(acc[j], a, a + (1 + j) * kOpBytes, kb, p.D, sf, sf + static_cast<uint32_t>(4 * (1 + j)));
           umma_commit(&bars.empty[st]);
           if (++st == kStages) { st = 0; ph ^= 1u; }
           if ((kb & 3) == 3 || kb == nb - 1) {
@@ -498,8 +531,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) break;
-        umma_commit(&bars.a_full[ab]);
-        if (++ab == kAccs) { ab = 0; aph ^= 1u; }
+#pragma unroll
+        for (int j = 0; j < kWideRun; ++j)
+          if (j < n) umma_commit(&bars.a_full[at[j]]);
       }
       umma_commit(&bars.drain);  // every MMA is done before TMEM can be released
       settle(&bars.drain, 0u, g);
@@ -509,14 +543,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     int ss = 0;
     uint32_t sph = 0;
     bool ok = true;
-    for (int64_t t = blockIdx.x; ok && t < p.ntiles; t += gridDim.x) {
+    for (int64_t t = blockIdx.x; ok && t < p.units; t += gridDim.x) {
       const TilePos tp = tile_pos(t, p);
       for (int k0 = 0; k0 < nb; k0 += 4) {
         if (!__all_sync(0xffffffffu, mbar_wait(&bars.sf_empty[ss], sph ^ 1u, g))) { ok = false; break; }
         tc_fence_after();
         const uint32_t a = su.tmem + lane_off + kSfBase + static_cast<uint32_t>(ss * kSfCols);
         store_scales(a, p.xs + static_cast<int64_t>(tp.b) * p.N * nb, tp.m0, p.N, nb, k0, lane);
-        store_scales(a + 4, p.cs + static_cast<int64_t>(tp.b) * p.K * nb, tp.n0, p.K, nb, k0, lane);
+        for (int j = 0; j < tp.n; ++j)
+          store_scales(a + static_cast<uint32_t>(4 * (1 + j)), p.cs + static_cast<int64_t>(tp.b) * p.K * nb,
+                       tp.n0 + j * kBN, p.K, nb, k0, lane);
         publish_scales(&bars.sf_full[ss], lane);
         if (++ss == kSfStages) { ss = 0; sph ^= 1u; }
       }
@@ -528,16 +564,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* bias = reinterpret_cast<float*>(su.epi + kEpiWarps * kStageBytes) + (warp - 8) * kBN;
     uint32_t aph = 0;
     int ab = 0;
-    for (int64_t t = blockIdx.x; t < p.ntiles; t += gridDim.x) {
-      const bool mine = ab == grp;
-      if (++ab == kAccs) ab = 0;
-      if (!mine) continue;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; ok && t < p.units; t += gridDim.x) {
       const TilePos tp = tile_pos(t, p);
-      const float4 bias4 = load_bias(p, tp.b, tp.n0, lane);
-      if (!__all_sync(0xffffffffu, mbar_wait(&bars.a_full[grp], aph, g))) break;
-      aph ^= 1u;
-      tc_fence_after();
-      emit_tile<BF16>(p, &smap, tp.b, tp.m0 + q4 * 32, tp.n0, tm, &bars.a_empty[grp], stage, bias, bias4, lane);
+      for (int j = 0; j < tp.n; ++j) {
+        const bool mine = ab == grp;
+        if (++ab == kAccs) ab = 0;
+        if (!mine) continue;
+        const int n0 = tp.n0 + j * kBN;
+        const float4 bias4 = load_bias(p, tp.b, n0, lane);
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars.a_full[grp], aph, g))) { ok = false; break; }
+        aph ^= 1u;
+        tc_fence_after();
+        emit_tile<BF16>(p, &smap, tp.b, tp.m0 + q4 * 32, n0, tm, &bars.a_empty[grp], stage, bias, bias4, lane);
+      }
     }
     stage_reusable(lane);
   }
@@ -562,9 +602,8 @@ cudaError_t launch_scores(const ScoresArgs& a, cudaStream_t s) {
   k.nt = (a.K + kBN - 1) / kBN;
   k.ntiles = k.mt * k.nt * a.B;
   k.S = a.S;
-  const int es = a.dtype == kDtypeBF16 ? 2 : 4;
   k.boxes = a.smap != nullptr;
-  k.pairs = es == 2 && a.K % 2 == 0 && reinterpret_cast<uintptr_t>(a.S) % 4 == 0;
+  k.pairs = a.K % 2 == 0 && reinterpret_cast<uintptr_t>(a.S) % 4 == 0;
   k.status = a.status;
   k.limit_ns = a.limit_ns;
   int dev = 0, nsm = 0;
@@ -574,15 +613,15 @@ cudaError_t launch_scores(const ScoresArgs& a, cudaStream_t s) {
   // blocks each leave room for (10 - 2 nb) / nb centroid tiles; shorter runs
   // where the units would not occupy every SM.
   const bool near = k.nb <= 2;
-  int64_t grid = k.ntiles;
+  k.runs = (k.nt + kWideRun - 1) / kWideRun;
+  k.units = a.B * k.mt * k.runs;
+  int64_t grid = k.units;
   if (near) {
     int64_t run = (kNearTiles - 2 * k.nb) / k.nb;
     if (run > k.nt) run = k.nt;
     while (run > 1 && a.B * ((k.nt + run - 1) / run) * k.mt < nsm) --run;
-    k.run = static_cast<int>(run);
     k.runs = (k.nt + run - 1) / run;
-    k.units = a.B * k.runs * k.mt;
-    grid = k.units;
+    grid = a.B * k.runs * k.mt;
   }
   const bool bf16 = a.dtype == kDtypeBF16;
   auto kern = near ? (bf16 ? k_scores_near<true> : k_scores_near<false>) : (bf16 ? k_scores_wide<true> : k_scores_wide<false>);

@@ -85,21 +85,47 @@ __device__ __forceinline__ void stage_reusable(int lane) {
   __syncwarp();
 }
 
-// The staged rows to rows of any alignment, words of W bytes (4 or 2) one per
-// lane, a row at a time: `rows` rows and `words` words of each are in range.
+// The staged rows, whole lines of 32 in-range rows, to rows of any alignment:
+// words of W bytes (4 or 2) one per lane, a row at a time.  Three instructions
+// to a row (they bound this path, not the sectors that rows share: carrying
+// those over from line to line took more).
 template <int W>
-__device__ __forceinline__ void store_words(const uint8_t* stage, uint8_t* dst, int64_t row_bytes, int rows, int words,
-                                            int lane) {
-  using E = typename std::conditional<W == 2, uint16_t, uint32_t>::type;
+__device__ __forceinline__ void store_lines(const uint8_t* stage, uint8_t* dst, uint32_t row_bytes, int lane) {
 #pragma unroll
   for (int h = 0; h < 4 / W; ++h) {
-    const int o = (h * 32 + lane) * W;
-    const bool in = h * 32 + lane < words;
-#pragma unroll 16
-    for (int r = 0; r < 32; ++r)
-      if (in && r < rows)
-        *reinterpret_cast<E*>(dst + r * row_bytes + o) =
-            *reinterpret_cast<const E*>(stage + r * 128 + (((o >> 4) ^ (r & 7)) << 4) + (o & 15));
+    const uint32_t o = static_cast<uint32_t>(h * 32 + lane) * W;
+    uint64_t to = reinterpret_cast<uint64_t>(dst) + o;
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) {
+      const uint32_t from = smem_addr(stage) + k * 128 + ((((o >> 4) ^ k) & 7) << 4) + (o & 15);
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) {
+        const uint64_t at = to + static_cast<uint64_t>(i * 8 + k) * row_bytes;
+        if (W == 4) {
+          uint32_t v;
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(from + i * 1024));
+          asm volatile("st.global.b32 [%0], %1;" ::"l"(at), "r"(v) : "memory");
+        } else {
+          uint16_t v;
+          asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(from + i * 1024));
+          asm volatile("st.global.b16 [%0], %1;" ::"l"(at), "h"(v) : "memory");
+        }
+      }
+    }
+  }
+}
+
+// The first n elements of each staged row, a row at a time.
+template <int ES>
+__device__ __forceinline__ void store_ragged(const uint8_t* stage, uint8_t* dst, int64_t row_bytes, int rows, int n,
+                                             int lane) {
+  using E = typename std::conditional<ES == 2, uint16_t, uint32_t>::type;
+  for (int c = lane; c < n; c += 32) {
+    const int o = c * ES;
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r)
+      *reinterpret_cast<E*>(dst + r * row_bytes + o) =
+          *reinterpret_cast<const E*>(stage + r * 128 + ((((o >> 4) ^ r) & 7) << 4) + (o & 15));
   }
 }
 
