@@ -413,8 +413,8 @@ int km_plan_describe(int op, int B, int64_t N, int D, int K, int dtype, int64_t 
  *
  * Points in 8 bits.  A set of points [B][N][D] is
  *   q      [B][N][ld] bytes, ld = D rounded up to a multiple of 16: e4m3
- *          values (16-byte aligned; the ld - D bytes behind a row are written
- *          as zero and never read);
+ *          values (16-byte aligned; km_quantize writes zeros to the ld - D bytes
+ *          behind a row, whose values do not matter);
  *   scale  [B][N][nb] bytes, nb = ceil(D / 128): e8m0 exponents, byte s
  *          standing for 2^(s - 127) and 255 for NaN;
  * and coordinate d of a point stands for q[d] * scale[d / 128].

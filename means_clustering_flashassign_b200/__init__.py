@@ -17,6 +17,7 @@ streamed in chunks).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import NamedTuple, Optional
@@ -69,6 +70,8 @@ def library_path() -> str:
 def library() -> ctypes.CDLL:
     """Load libkm.so (building it first if the sources are newer)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.LIB
@@ -748,6 +751,7 @@ class Balance(NamedTuple):
     picks: int
 
 
+@functools.lru_cache(maxsize=4096)
 def soft_workspace_size(op: int, B: int, N: int, D: int, K: int, dtype: int) -> int:
     n = library().km_soft_workspace_size(op, B, N, D, K, dtype)
     if n == 0:
@@ -757,21 +761,35 @@ def soft_workspace_size(op: int, B: int, N: int, D: int, K: int, dtype: int) -> 
 
 class _on:
     """Device and stream of a call: outputs and workspaces allocated inside
-    belong to the stream the kernels run on."""
+    belong to the stream the kernels run on, and .raw is that stream.  Nothing
+    is switched where the caller's device and stream are meant: the calls of a
+    training or serving loop take microseconds."""
+
+    __slots__ = ("_d", "_s", "raw")
 
     def __init__(self, device, stream):
-        self._d = torch.cuda.device(device)
-        self._s = torch.cuda.stream(stream) if stream is not None else None
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the points are on {device}")
+        self._d = None if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
+        self._s = None if stream is None else torch.cuda.stream(stream)
+        self.raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
     def __enter__(self):
-        self._d.__enter__()
+        if self._d is not None:
+            self._d.__enter__()
         if self._s is not None:
             self._s.__enter__()
+        return self.raw
 
     def __exit__(self, *a):
         if self._s is not None:
             self._s.__exit__(*a)
-        self._d.__exit__(*a)
+        if self._d is not None:
+            self._d.__exit__(*a)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _soft_workspace(op, B, N, D, K, dtype, device, workspace):
@@ -796,7 +814,7 @@ def _new_quantized(lead, D, device) -> Quantized:
     ld = (D + 15) // 16 * 16
     data = torch.empty(*lead, ld, dtype=torch.float8_e4m3fn, device=device)
     scale = torch.empty(*lead, (D + 127) // 128, dtype=torch.float8_e8m0fnu, device=device)
-    return Quantized(data[..., :D], scale)
+    return Quantized(data if ld == D else data[..., :D], scale)
 
 
 def _check_quantized(q, name: str, device=None):
@@ -812,16 +830,16 @@ def _check_quantized(q, name: str, device=None):
     B, N, D, batched = _shape3(data, name)
     ld = (D + 15) // 16 * 16
     want = ((N * ld, ld, 1) if batched else (ld, 1))
-    if any(n > 1 and s != w for n, s, w in zip(data.shape, data.stride(), want)):
+    if data.stride() != want and any(n > 1 and s != w for n, s, w in zip(data.shape, data.stride(), want)):
         raise ValueError(f"rows of {name}.data must be dense and {ld} bytes apart")
-    if data.numel() and data.data_ptr() % 16:
+    if data.data_ptr() % 16 and data.numel():
         raise ValueError(f"{name}.data must be 16-byte aligned")
-    if data.numel() and data.untyped_storage().nbytes() - data.storage_offset() < B * N * ld:
+    if ld != D and data.numel() and data.untyped_storage().nbytes() - data.storage_offset() < B * N * ld:
         raise ValueError(f"the last row of {name}.data must have {ld} bytes")
-    shp = (*data.shape[:-1], (D + 127) // 128)
-    _check_tensor(scale, f"{name}.scale", data.device, None, shp)
-    if device is not None and data.device != device:
-        raise ValueError(f"{name} is on {data.device}, the points are on {device}")
+    dev = data.device
+    _check_tensor(scale, f"{name}.scale", dev, None, (*data.shape[:-1], (D + 127) // 128))
+    if device is not None and dev != device:
+        raise ValueError(f"{name} is on {dev}, the points are on {device}")
     return B, N, D, batched
 
 
@@ -832,14 +850,15 @@ def quantize(X: torch.Tensor, *, out: Optional[Quantized] = None, stream=None) -
     _contig_cuda(X, "X")
     B, N, D, _ = _shape3(X, "X")
     dt = _dtype_code(X)
-    _check_stream(stream, X.device)
-    with _on(X.device, stream):
+    dev = X.device
+    with _on(dev, stream) as raw:
         if out is None:
-            out = _new_quantized(X.shape[:-1], D, X.device)
-        elif out.data.shape != X.shape:
-            raise ValueError(f"out must have shape {tuple(X.shape)}, got {tuple(out.data.shape)}")
-        _check_quantized(out, "out", X.device)
-        _check(library().km_quantize(_ptr(X), B, N, D, dt, _ptr(out.data), _ptr(out.scale), _stream(None)))
+            out = _new_quantized(X.shape[:-1], D, dev)
+        else:
+            if out.data.shape != X.shape:
+                raise ValueError(f"out must have shape {tuple(X.shape)}, got {tuple(out.data.shape)}")
+            _check_quantized(out, "out", dev)
+        _check(library().km_quantize(X.data_ptr(), B, N, D, dt, out.data.data_ptr(), out.scale.data_ptr(), raw))
     return out
 
 
@@ -847,23 +866,23 @@ def dequantize(q: Quantized, dtype: torch.dtype = torch.bfloat16, *, out=None, s
     """The values 8-bit points stand for, in bf16 or f32 (exact in both)."""
     B, N, D, _ = _check_quantized(q, "q")
     dt = _soft_dtype(dtype)
-    dev = q.data.device
-    _check_stream(stream, dev)
-    with _on(dev, stream):
+    data, scale = q
+    dev = data.device
+    with _on(dev, stream) as raw:
         if out is None:
-            out = torch.empty(q.data.shape, dtype=dtype, device=dev)
-        _check_tensor(out, "out", dev, dtype, q.data.shape)
-        _check(library().km_dequantize(_ptr(q.data), _ptr(q.scale), B, N, D, dt, _ptr(out), _stream(None)))
+            out = torch.empty(data.shape, dtype=dtype, device=dev)
+        else:
+            _check_tensor(out, "out", dev, dtype, data.shape)
+        _check(library().km_dequantize(data.data_ptr(), scale.data_ptr(), B, N, D, dt, out.data_ptr(), raw))
     return out
 
 
-def _score_args(X, C, stream):
+def _score_args(X, C):
     B, N, D, batched = _check_quantized(X, "X")
     dev = X.data.device
     Bc, K, Dc, batched_c = _check_quantized(C, "C", dev)
     if Bc != B or Dc != D or batched_c != batched:
         raise ValueError("C must match X in batch and D")
-    _check_stream(stream, dev)
     return B, N, D, K, batched, dev
 
 
@@ -873,18 +892,19 @@ def scores(X: Quantized, C: Quantized, *, bias: Optional[torch.Tensor] = None, a
     every pair, (N, K) or (B, N, K) in `dtype` (bf16 or f32).  bias float32 (K,)
     or (B, K).  alpha = 2 / t and bias = -|c|^2 / t give the logits of a soft
     assignment by distance."""
-    B, N, D, K, batched, dev = _score_args(X, C, stream)
+    B, N, D, K, batched, dev = _score_args(X, C)
     dt = _soft_dtype(dtype)
     shp = (B, N, K) if batched else (N, K)
     if bias is not None:
         _check_tensor(bias, "bias", dev, torch.float32, (B, K) if batched else (K,))
-    with _on(dev, stream):
+    with _on(dev, stream) as raw:
         if out is None:
             out = torch.empty(shp, dtype=dtype, device=dev)
-        _check_tensor(out, "out", dev, dtype, shp)
+        else:
+            _check_tensor(out, "out", dev, dtype, shp)
         ws = _soft_workspace(SOFT_SCORES, B, N, D, K, dt, dev, workspace)
-        _check(library().km_scores(_ptr(X.data), _ptr(X.scale), _ptr(C.data), _ptr(C.scale), _ptr(bias), alpha, B, N, D,
-                                   K, dt, _ptr(out), _ptr(ws), ws.numel(), _stream(None)))
+        _check(library().km_scores(X.data.data_ptr(), X.scale.data_ptr(), C.data.data_ptr(), C.scale.data_ptr(),
+                                   _addr(bias), alpha, B, N, D, K, dt, out.data_ptr(), ws.data_ptr(), ws.numel(), raw))
     return out
 
 
@@ -897,7 +917,7 @@ def scores_grad(dS: torch.Tensor, X: Quantized, C: Quantized, *, alpha: float = 
     Returns (dX in `dtype`, by default dS's, dC float32, dbias float32), None for
     those not wanted."""
     _contig_cuda(dS, "dS")
-    B, N, D, K, batched, dev = _score_args(X, C, stream)
+    B, N, D, K, batched, dev = _score_args(X, C)
     _check_tensor(dS, "dS", dev, None, (B, N, K) if batched else (N, K))
     dt = _dtype_code(dS)
     dtype = dS.dtype if dtype is None else dtype
@@ -905,14 +925,14 @@ def scores_grad(dS: torch.Tensor, X: Quantized, C: Quantized, *, alpha: float = 
     if not (want_dX or want_dC or want_dbias):
         raise ValueError("one of dX, dC and dbias must be wanted")
     lead = (B,) if batched else ()
-    with _on(dev, stream):
+    with _on(dev, stream) as raw:
         dX = torch.empty((*lead, N, D), dtype=dtype, device=dev) if want_dX else None
         dC = torch.empty((*lead, K, D), dtype=torch.float32, device=dev) if want_dC else None
         db = torch.empty((*lead, K), dtype=torch.float32, device=dev) if want_dbias else None
         ws = _soft_workspace(SOFT_SCORES_GRAD, B, N, D, K, dt, dev, workspace)
-        _check(library().km_scores_grad(_ptr(dS), _ptr(X.data), _ptr(X.scale), _ptr(C.data), _ptr(C.scale), alpha, B, N,
-                                        D, K, dt, dxt, _ptr(dX), _ptr(dC), _ptr(db), _ptr(ws), ws.numel(),
-                                        _stream(None)))
+        _check(library().km_scores_grad(dS.data_ptr(), X.data.data_ptr(), X.scale.data_ptr(), C.data.data_ptr(),
+                                        C.scale.data_ptr(), alpha, B, N, D, K, dt, dxt, _addr(dX), _addr(dC), _addr(db),
+                                        ws.data_ptr(), ws.numel(), raw))
     return dX, dC, db
 
 
@@ -933,23 +953,24 @@ def balance(S: torch.Tensor, idx: torch.Tensor, *, valid: Optional[torch.Tensor]
     _contig_cuda(S, "S")
     B, N, K, batched = _shape3(S, "S")
     dt = _dtype_code(S)
+    dev = S.device
     lead = (B, N) if batched else (N,)
-    T = idx.shape[-1] if idx.dim() == len(lead) + 1 else 1
+    many = idx.dim() == len(lead) + 1
+    T = idx.shape[-1] if many else 1
     if T < 1:
         raise ValueError("idx must hold at least one pick per point")
-    _check_tensor(idx, "idx", S.device, torch.int32, (*lead, T) if idx.dim() == len(lead) + 1 else lead)
-    valid = _valid_mask(valid, lead, S.device)
-    _check_stream(stream, S.device)
-    dev = S.device
-    with _on(dev, stream):
+    _check_tensor(idx, "idx", dev, torch.int32, (*lead, T) if many else lead)
+    valid = _valid_mask(valid, lead, dev)
+    with _on(dev, stream) as raw:
         loss = torch.empty(B, dtype=torch.float32, device=dev)
         counts = torch.empty((B, K) if batched else (K,), dtype=torch.int32, device=dev)
         rows = torch.empty(B, dtype=torch.int32, device=dev)
         lse = torch.empty(lead, dtype=torch.float32, device=dev)
         dot = torch.empty(lead, dtype=torch.float32, device=dev)
         ws = _soft_workspace(SOFT_BALANCE, B, N, 1, K, dt, dev, workspace)
-        _check(library().km_balance(_ptr(S), _ptr(idx), _ptr(valid), B, N, K, T, dt, _ptr(loss), _ptr(counts),
-                                    _ptr(rows), _ptr(lse), _ptr(dot), _ptr(ws), ws.numel(), _stream(None)))
+        _check(library().km_balance(S.data_ptr(), idx.data_ptr(), _addr(valid), B, N, K, T, dt, loss.data_ptr(),
+                                    counts.data_ptr(), rows.data_ptr(), lse.data_ptr(), dot.data_ptr(), ws.data_ptr(),
+                                    ws.numel(), raw))
     return Balance(loss, counts, rows, lse, dot, T)
 
 
@@ -970,13 +991,14 @@ def balance_grad(S: torch.Tensor, bal: Balance, *, grad: Optional[torch.Tensor] 
     valid = _valid_mask(valid, lead, dev)
     if grad is not None:
         _check_tensor(grad, "grad", dev, torch.float32, (B,))
-    _check_stream(stream, dev)
-    with _on(dev, stream):
+    with _on(dev, stream) as raw:
         if out is None:
             out = torch.empty_like(S)
-        _check_tensor(out, "out", dev, S.dtype, S.shape)
-        if out.numel() and out.data_ptr() == S.data_ptr():
-            raise ValueError("out must not be S")
-        _check(library().km_balance_grad(_ptr(S), _ptr(valid), _ptr(bal.counts), _ptr(bal.rows), _ptr(bal.lse),
-                                         _ptr(bal.dot), _ptr(grad), B, N, K, bal.picks, dt, _ptr(out), _stream(None)))
+        else:
+            _check_tensor(out, "out", dev, S.dtype, S.shape)
+            if out.numel() and out.data_ptr() == S.data_ptr():
+                raise ValueError("out must not be S")
+        _check(library().km_balance_grad(S.data_ptr(), _addr(valid), bal.counts.data_ptr(), bal.rows.data_ptr(),
+                                         bal.lse.data_ptr(), bal.dot.data_ptr(), _addr(grad), B, N, K, bal.picks, dt,
+                                         out.data_ptr(), raw))
     return out

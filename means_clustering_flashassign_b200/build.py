@@ -21,7 +21,7 @@ OBJ_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkm.so")
 SOURCES = ["km_api.cu", "k_prep.cu", "k_assign.cu", "k_sort.cu", "k_update.cu", "km_noalloc.cu", "k_ablation.cu",
            "km_soft.cu", "k_quant.cu", "k_scores.cu", "k_grad.cu", "k_balance.cu"]
-HEADERS = ["km_internal.h", "km_ptx.cuh", "km_rows.cuh", "km_soft.h", "km_tile.cuh"]
+HEADERS = ["km_internal.h", "km_ptx.cuh", "km_rows.cuh", "km_soft.h", "km_tile.cuh", "km_e4m3.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-I", os.path.join(ROOT, "include")]

@@ -26,6 +26,7 @@
 // Structure: warp 0 TMA, warp 1 MMA, warps 2..9 epilogue, warps 10..17 column
 // sums (dbias, from the staged dS slices of the dC product: float32 over 16
 // points, those joined in float64).  Every wait is bounded in time.
+#include "km_e4m3.cuh"
 #include "km_internal.h"
 #include "km_soft.h"
 #include "km_tile.cuh"
@@ -138,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  pdl_wait();  // the operands come from k_grad_prep
   const WaitGuard g{p.status, abort_flag, p.limit_ns};
   const int64_t grp = blockIdx.x / p.group;
   const int me = static_cast<int>(blockIdx.x - grp * p.group);
@@ -425,11 +427,12 @@ __device__ __forceinline__ Acc join_pieces(const float* part, int pieces, int64_
   for (int s = ty; s < pieces; s += kJoinY) v += part[static_cast<int64_t>(s) * stride + i];
   return v;
 }
-__global__ void __launch_bounds__(kT) k_grad_join(const float* __restrict__ cpart, int csplits, int64_t nc,
-                                                  float* __restrict__ dC, const float* __restrict__ bpart, int bsplits,
+__global__ void __launch_bounds__(kT) k_grad_join(const float* cpart, int csplits, int64_t nc,
+                                                  float* __restrict__ dC, const float* bpart, int bsplits,
                                                   int64_t nb, float* __restrict__ dbias) {
   __shared__ double sum[kJoinY][kJoinX];
   const int tx = threadIdx.x % kJoinX, ty = threadIdx.x / kJoinX;
+  pdl_wait();
   for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kJoinX; i0 < nc + nb;
        i0 += static_cast<int64_t>(gridDim.x) * kJoinX) {
     const int64_t i = i0 + tx;
@@ -448,25 +451,114 @@ __global__ void __launch_bounds__(kT) k_grad_join(const float* __restrict__ cpar
   }
 }
 
-// hi + mid + lo = x: each piece is the bf16 nearest to what is left.
-template <bool BF16>
-__global__ void __launch_bounds__(kT) k_split_planes(const void* __restrict__ dS, int64_t n, int K, int64_t ld,
-                                                     int64_t plane, __nv_bfloat16* __restrict__ out) {
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kT + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * kT) {
-    const int64_t row = i / K;
-    const int64_t o = row * ld + (i - row * K);
-    if constexpr (BF16) {
-      out[o] = static_cast<const __nv_bfloat16*>(dS)[i];
-    } else {
-      float x = static_cast<const float*>(dS)[i];
+struct PrepK {
+  GradPrepArgs a;
+  unsigned cblocks, xblocks;   // blocks of the centroids' and the points' part
+  int64_t cpieces, xpieces, spieces;
+};
+
+// Pieces of 8 coordinates (16 bytes of bf16 out) of an operand, four in flight.
+__device__ __forceinline__ void prep_values(const uint8_t* q, const uint8_t* scale, __nv_bfloat16* out, int64_t pieces,
+                                            int D, int64_t ldd, unsigned blk, unsigned nblk) {
+  constexpr int kU = 4;
+  const int gpr = static_cast<int>(ldd / 8), nb = (D + kQBlock - 1) / kQBlock;
+  const int64_t ld = (static_cast<int64_t>(D) + 15) / 16 * 16;
+  const bool small = pieces < (int64_t(1) << 31);  // a 32-bit division is much the cheaper one
+  for (int64_t base = static_cast<int64_t>(blk) * (kT * kU) + threadIdx.x; base < pieces;
+       base += static_cast<int64_t>(nblk) * (kT * kU)) {
+    uint2 u[kU];
+    float s[kU];
+    int64_t to[kU];
 #pragma unroll
-      for (int pl = 0; pl < 3; ++pl) {
-        const __nv_bfloat16 h = __float2bfloat16_rn(x);
-        out[pl * plane + o] = h;
-        x -= __bfloat162float(h);
-      }
+    for (int k = 0; k < kU; ++k) {
+      const int64_t at = base + k * kT;
+      to[k] = -1;
+      if (at >= pieces) continue;
+      const int64_t row = small ? static_cast<int64_t>(static_cast<uint32_t>(at) / static_cast<uint32_t>(gpr)) : at / gpr;
+      const int c = static_cast<int>(at - row * gpr) * 8;
+      u[k] = __ldcs(reinterpret_cast<const uint2*>(q + row * ld + c));
+      s[k] = e8m0(__ldg(scale + row * nb + c / kQBlock));
+      to[k] = row * ldd + c;
     }
+#pragma unroll
+    for (int k = 0; k < kU; ++k)
+      if (to[k] >= 0) *reinterpret_cast<uint4*>(out + to[k]) = e4m3x8_bf16(u[k], s[k]);
+  }
+}
+
+// bf16 dS to rows of ldk elements: 8 columns a piece, from the 32-bit words
+// that hold them (a row of an odd width starts in the middle of one).
+__device__ __forceinline__ void prep_copy(const uint32_t* src, uint4* out, int64_t pieces, int64_t rows, int K,
+                                          int64_t ldk, unsigned blk, unsigned nblk) {
+  const int gpr = static_cast<int>(ldk / 8);
+  const int64_t total = rows * K;
+  for (int64_t at = static_cast<int64_t>(blk) * kT + threadIdx.x; at < pieces; at += static_cast<int64_t>(nblk) * kT) {
+    const int64_t row = pieces < (int64_t(1) << 31)
+                            ? static_cast<int64_t>(static_cast<uint32_t>(at) / static_cast<uint32_t>(gpr)) : at / gpr;
+    const int64_t e = row * K + (at - row * gpr) * 8;  // first element, in word e / 2
+    uint32_t w[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+      const int64_t h = (e & ~int64_t(1)) + 2 * i;  // nothing of a word behind the last element is read
+      w[i] = 0;
+      if (h + 1 < total) w[i] = __ldg(src + h / 2);
+      else if (h < total) w[i] = reinterpret_cast<const uint16_t*>(src)[h];
+    }
+    if (e & 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    }
+    out[at] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// float32 dS as hi + mid + lo, each piece the bf16 nearest to what is left: 4
+// columns at a time.
+__device__ __forceinline__ void prep_planes(const float* src, __nv_bfloat16* out, int64_t pieces, int64_t rows, int K,
+                                            int64_t ldk, unsigned blk, unsigned nblk) {
+  const int gpr = static_cast<int>(ldk / 4);
+  const bool vec = K % 4 == 0;
+  for (int64_t at = static_cast<int64_t>(blk) * kT + threadIdx.x; at < pieces; at += static_cast<int64_t>(nblk) * kT) {
+    const int64_t row = pieces < (int64_t(1) << 31)
+                            ? static_cast<int64_t>(static_cast<uint32_t>(at) / static_cast<uint32_t>(gpr)) : at / gpr;
+    const int c = static_cast<int>(at - row * gpr) * 4;
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    if (vec) {
+      if (c < K) {
+        const float4 v = __ldcs(reinterpret_cast<const float4*>(src + row * K + c));
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i < K) x[i] = src[row * K + c + i];
+    }
+#pragma unroll
+    for (int pl = 0; pl < 3; ++pl) {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+      *reinterpret_cast<uint2*>(out + (pl * rows + row) * ldk + c) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+      const float2 fa = __bfloat1622float2(a), fb = __bfloat1622float2(b);
+      x[0] -= fa.x, x[1] -= fa.y, x[2] -= fb.x, x[3] -= fb.y;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kT) k_grad_prep(const __grid_constant__ PrepK p) {
+  const GradPrepArgs& a = p.a;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
+  unsigned blk = blockIdx.x;
+  if (blk < p.cblocks) {
+    prep_values(a.cq, a.cs, static_cast<__nv_bfloat16*>(a.cop), p.cpieces, a.D, a.ldd, blk, p.cblocks);
+  } else if ((blk -= p.cblocks) < p.xblocks) {
+    prep_values(a.xq, a.xs, static_cast<__nv_bfloat16*>(a.xop), p.xpieces, a.D, a.ldd, blk, p.xblocks);
+  } else if (p.spieces) {
+    blk -= p.xblocks;
+    const unsigned n = gridDim.x - p.cblocks - p.xblocks;
+    if (a.dtype == kDtypeBF16)
+      prep_copy(static_cast<const uint32_t*>(a.dS), static_cast<uint4*>(a.planes), p.spieces, a.xrows, a.K, a.ldk, blk, n);
+    else
+      prep_planes(static_cast<const float*>(a.dS), static_cast<__nv_bfloat16*>(a.planes), p.spieces, a.xrows, a.K, a.ldk, blk, n);
   }
 }
 
@@ -475,21 +567,14 @@ unsigned grid_of(int64_t n) {
   return static_cast<unsigned>(b < 148 * 16 ? b : 148 * 16);
 }
 
-cudaError_t plain_launch() {
-  chain_break();
-  if (fault_hit(kFaultLaunch)) return cudaErrorLaunchFailure;
-  count_launch();
-  return cudaSuccess;
-}
-
 template <int KT, bool OUT_BF16, bool WX, bool WC, bool WB>
 cudaError_t grad_t(const GradArgs& a, const GradK& k, cudaStream_t s) {
   auto kern = k_grad<KT, OUT_BF16, WX, WC, WB>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
   if (e != cudaSuccess) return e;
-  if ((e = plain_launch()) != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(k.groups * k.group), kThreads, kSmem, s>>>(*a.ds_x, *a.ds_c, *a.cmap, *a.xmap, k);
-  return cudaGetLastError();
+  count_launch();
+  return launch_chained(kern, dim3(static_cast<unsigned>(k.groups * k.group)), dim3(kThreads), kSmem, s, *a.ds_x, *a.ds_c,
+                        *a.cmap, *a.xmap, k);
 }
 
 template <int KT, bool OUT_BF16>
@@ -572,20 +657,26 @@ cudaError_t launch_grad(const GradArgs& a, cudaStream_t s) {
 
 cudaError_t launch_grad_join(const float* cpart, int csplits, int64_t nc, float* dC, const float* bpart, int bsplits,
                              int64_t nb, float* dbias, cudaStream_t s) {
-  cudaError_t e = plain_launch();
-  if (e != cudaSuccess) return e;
-  k_grad_join<<<grid_of((nc + nb) * kJoinY), kT, 0, s>>>(cpart, csplits, nc, dC, bpart, bsplits, nb, dbias);
-  return cudaGetLastError();
+  count_launch();
+  return launch_chained(k_grad_join, dim3(grid_of((nc + nb) * kJoinY)), dim3(kT), 0, s, cpart, csplits, nc, dC, bpart,
+                        bsplits, nb, dbias);
 }
 
-cudaError_t launch_split_planes(const void* dS, int dtype, int64_t rows, int K, int64_t ld, void* planes,
-                                cudaStream_t s) {
-  cudaError_t e = plain_launch();
-  if (e != cudaSuccess) return e;
-  auto* o = static_cast<__nv_bfloat16*>(planes);
-  if (dtype == kDtypeBF16) k_split_planes<true><<<grid_of(rows * K), kT, 0, s>>>(dS, rows * K, K, ld, rows * ld, o);
-  else k_split_planes<false><<<grid_of(rows * K), kT, 0, s>>>(dS, rows * K, K, ld, rows * ld, o);
-  return cudaGetLastError();
+cudaError_t launch_grad_prep(const GradPrepArgs& a, cudaStream_t s) {
+  PrepK k{};
+  k.a = a;
+  auto blocks = [](int64_t pieces, int per) {
+    const int64_t b = (pieces + kT * per - 1) / (kT * per);
+    return static_cast<unsigned>(b < 148 * 8 ? b : 148 * 8);
+  };
+  k.cpieces = a.cop ? a.crows * (a.ldd / 8) : 0;
+  k.xpieces = a.xop ? a.xrows * (a.ldd / 8) : 0;
+  k.spieces = a.planes ? a.xrows * (a.ldk / (a.dtype == kDtypeBF16 ? 8 : 4)) : 0;
+  k.cblocks = blocks(k.cpieces, 4);
+  k.xblocks = blocks(k.xpieces, 4);
+  const unsigned grid = k.cblocks + k.xblocks + blocks(k.spieces, 1);
+  count_launch();
+  return launch_chained(k_grad_prep, dim3(grid ? grid : 1), dim3(kT), 0, s, k);
 }
 
 }  // namespace km

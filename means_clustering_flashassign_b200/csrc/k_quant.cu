@@ -13,11 +13,10 @@
 //
 // Both directions are one pass over memory; a thread has the loads of four
 // pieces in flight before it uses the first.
-#include <cuda_bf16.h>
-#include <cuda_fp8.h>
 
 #include <type_traits>
 
+#include "km_e4m3.cuh"
 #include "km_internal.h"
 #include "km_soft.h"
 
@@ -143,11 +142,6 @@ __global__ void __launch_bounds__(kQThreads) k_quantize(const elem_t<BF16>* __re
   }
 }
 
-// The value of an e8m0 scale byte.
-__device__ __forceinline__ float e8m0(uint32_t b) {
-  return __uint_as_float(b == 255u ? 0x7fc00000u : (b ? b << 23 : 0x00400000u));
-}
-
 // Coordinates per piece of k_dequantize: 16 bytes of output, so that a warp's
 // store instruction writes whole sectors (two 16-byte stores to each 32 bytes
 // of a lane's own, taken apart, moved 2.5 times the sectors through L2).
@@ -159,7 +153,7 @@ constexpr int kDU = 4;
 template <bool BF16, bool VEC, typename I>
 __global__ void __launch_bounds__(kQThreads) k_dequantize(const uint8_t* __restrict__ q,
                                                           const uint8_t* __restrict__ scale, I groups, int gpr, int nb,
-                                                          int D, int64_t ld, int64_t ld_out,
+                                                          int D, int64_t ld,
                                                           elem_t<BF16>* __restrict__ X) {
   constexpr int kDE = kDE_of<BF16>;
   const int64_t step = static_cast<int64_t>(gridDim.x) * (kQThreads * kDU);
@@ -188,29 +182,20 @@ __global__ void __launch_bounds__(kQThreads) k_dequantize(const uint8_t* __restr
 #pragma unroll
     for (int k = 0; k < kDU; ++k) {
       if (row[k] < 0) continue;
-      float v[kDE];
-#pragma unroll
-      for (int i = 0; i < kDE / 2; ++i) {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-            static_cast<__nv_fp8x2_storage_t>(u[k][i / 2] >> (16 * (i & 1))), __NV_E4M3);
-        const float2 f = __half22float2(__half2(h));
-        v[2 * i] = f.x * s[k];
-        v[2 * i + 1] = f.y * s[k];
-      }
-      elem_t<BF16>* out = X + row[k] * ld_out + c0[k];
-      if (VEC) {  // whole pieces: D is a multiple of 8
-        if constexpr (BF16) {
-          uint32_t o[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            o[i] = *reinterpret_cast<const uint32_t*>(&b2);
-          }
-          *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
-        } else {
-          *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
-        }
+      elem_t<BF16>* out = X + row[k] * D + c0[k];
+      if constexpr (VEC && BF16) {  // whole pieces: D is a multiple of 8
+        *reinterpret_cast<uint4*>(out) = e4m3x8_bf16(make_uint2(u[k][0], u[k][1]), s[k]);
+      } else if constexpr (VEC) {
+        const float2 a = e4m3x2(u[k][0], s[k]), b = e4m3x2(u[k][0] >> 16, s[k]);
+        *reinterpret_cast<float4*>(out) = make_float4(a.x, a.y, b.x, b.y);
       } else {
+        float v[kDE];
+#pragma unroll
+        for (int i = 0; i < kDE / 2; ++i) {
+          const float2 f = e4m3x2(u[k][i / 2] >> (16 * (i & 1)), s[k]);
+          v[2 * i] = f.x;
+          v[2 * i + 1] = f.y;
+        }
 #pragma unroll
         for (int i = 0; i < kDE; ++i) {
           if (c0[k] + i >= D) break;
@@ -248,16 +233,16 @@ void quantize_d(const void* X, int64_t blocks, int nb, int D, uint8_t* q, uint8_
 }
 
 template <bool BF16, bool VEC>
-void dequantize_t(const uint8_t* q, const uint8_t* scale, int64_t rows, int D, int64_t ld_out, void* X, cudaStream_t s) {
+void dequantize_t(const uint8_t* q, const uint8_t* scale, int64_t rows, int D, void* X, cudaStream_t s) {
   const int gpr = (D + kDE_of<BF16> - 1) / kDE_of<BF16>;
   const int64_t groups = rows * gpr;
   const unsigned grid = grid_for(groups, kQThreads * kDU);
   auto* o = static_cast<elem_t<BF16>*>(X);
   if (groups < (int64_t(1) << 31))
     k_dequantize<BF16, VEC, uint32_t><<<grid, kQThreads, 0, s>>>(q, scale, static_cast<uint32_t>(groups), gpr, q_blocks(D),
-                                                                 D, q_ld(D), ld_out, o);
+                                                                 D, q_ld(D), o);
   else
-    k_dequantize<BF16, VEC, int64_t><<<grid, kQThreads, 0, s>>>(q, scale, groups, gpr, q_blocks(D), D, q_ld(D), ld_out, o);
+    k_dequantize<BF16, VEC, int64_t><<<grid, kQThreads, 0, s>>>(q, scale, groups, gpr, q_blocks(D), D, q_ld(D), o);
 }
 
 }  // namespace
@@ -277,17 +262,17 @@ cudaError_t launch_quantize(const void* X, int dtype, int64_t rows, int D, uint8
   return cudaGetLastError();
 }
 
-cudaError_t launch_dequantize(const uint8_t* q, const uint8_t* scale, int dtype, int64_t rows, int D, int64_t ld_out,
-                              void* X, cudaStream_t s) {
+cudaError_t launch_dequantize(const uint8_t* q, const uint8_t* scale, int dtype, int64_t rows, int D, void* X,
+                              cudaStream_t s) {
   if (rows == 0) return cudaSuccess;
   chain_break();
   if (fault_hit(kFaultLaunch)) return cudaErrorLaunchFailure;
   count_launch();
-  const bool vec = D % 8 == 0 && ld_out % 8 == 0 && reinterpret_cast<uintptr_t>(X) % 16 == 0;
+  const bool vec = D % 8 == 0 && reinterpret_cast<uintptr_t>(X) % 16 == 0;
   if (dtype == kDtypeBF16)
-    vec ? dequantize_t<true, true>(q, scale, rows, D, ld_out, X, s) : dequantize_t<true, false>(q, scale, rows, D, ld_out, X, s);
+    vec ? dequantize_t<true, true>(q, scale, rows, D, X, s) : dequantize_t<true, false>(q, scale, rows, D, X, s);
   else
-    vec ? dequantize_t<false, true>(q, scale, rows, D, ld_out, X, s) : dequantize_t<false, false>(q, scale, rows, D, ld_out, X, s);
+    vec ? dequantize_t<false, true>(q, scale, rows, D, X, s) : dequantize_t<false, false>(q, scale, rows, D, X, s);
   return cudaGetLastError();
 }
 

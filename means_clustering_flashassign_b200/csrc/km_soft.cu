@@ -2,6 +2,7 @@
 // include/km.h): argument checks, workspace carving, tensor maps and launch
 // sequences of the 8-bit points, the scores, their gradients and the balance
 // loss.
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 
@@ -50,6 +51,20 @@ int check_shape(int B, int64_t N, int D, int K, int dtype) {
   if (D > kMaxD) return sfail(KM_ERR_UNSUPPORTED, "D=%d above 2^16", D);
   if (K > kMaxK) return sfail(KM_ERR_UNSUPPORTED, "K=%d above 2^20", K);
   return KM_OK;
+}
+
+// KM_OK on an sm_100 device.  A device's answer is looked up once: the calls
+// of a serving loop take microseconds.
+int check_device_once() {
+  constexpr int kMax = 64;
+  static std::atomic<bool> good[kMax];
+  int dev = 0;
+  SOFT_CUDA(cudaGetDevice(&dev));
+  const bool known = dev >= 0 && dev < kMax;
+  if (known && good[dev].load(std::memory_order_relaxed)) return KM_OK;
+  const int r = api_check_device();
+  if (r == KM_OK && known) good[dev].store(true, std::memory_order_relaxed);
+  return r;
 }
 
 // Workspace layout of an operator (offsets in bytes; the status word is at 0).
@@ -106,7 +121,7 @@ int soft_prepare(SoftCtx& c, int op, int B, int64_t N, int D, int K, int dtype, 
   if (reinterpret_cast<uintptr_t>(ws) % kAlign) return sfail(KM_ERR_WORKSPACE, "workspace must be 256-byte aligned");
   if (ws_bytes < c.l.total)
     return sfail(KM_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, c.l.total);
-  r = api_check_device();
+  r = check_device_once();
   if (r != KM_OK) return r;
   c.ws = static_cast<uint8_t*>(ws);
   c.s = static_cast<cudaStream_t>(stream);
@@ -157,7 +172,7 @@ int km_quantize(const void* X, int B, int64_t N, int D, int dtype, uint8_t* q, u
     return sfail(KM_ERR_INVALID_ARG, "X, q and scale are required");
   }
   if (!aligned16(q)) return sfail(KM_ERR_INVALID_ARG, "q must be 16-byte aligned");
-  if ((r = api_check_device()) != KM_OK) return r;
+  if ((r = check_device_once()) != KM_OK) return r;
   SOFT_CUDA(launch_quantize(X, dtype, static_cast<int64_t>(B) * N, D, q, scale, static_cast<cudaStream_t>(stream)));
   return KM_OK;
 }
@@ -172,9 +187,8 @@ int km_dequantize(const uint8_t* q, const uint8_t* scale, int B, int64_t N, int 
     return sfail(KM_ERR_INVALID_ARG, "q, scale and X are required");
   }
   if (!aligned16(q)) return sfail(KM_ERR_INVALID_ARG, "q must be 16-byte aligned");
-  if ((r = api_check_device()) != KM_OK) return r;
-  SOFT_CUDA(launch_dequantize(q, scale, dtype, static_cast<int64_t>(B) * N, D, D, X,
-                              static_cast<cudaStream_t>(stream)));
+  if ((r = check_device_once()) != KM_OK) return r;
+  SOFT_CUDA(launch_dequantize(q, scale, dtype, static_cast<int64_t>(B) * N, D, X, static_cast<cudaStream_t>(stream)));
   return KM_OK;
 }
 
@@ -217,8 +231,8 @@ int km_scores_grad(const void* dS, const uint8_t* xq, const uint8_t* xs, const u
   int r = soft_prepare(c, KM_SOFT_SCORES_GRAD, B, N, D, K, dtype, workspace, workspace_bytes, stream);
   if (r != KM_OK) return r;
   const Layout& l = c.l;
-  SOFT_CUDA(cudaMemsetAsync(c.status(), 0, sizeof(unsigned int), c.s));
   if (N == 0) {  // empty sums
+    SOFT_CUDA(cudaMemsetAsync(c.status(), 0, sizeof(unsigned int), c.s));
     if (dC) SOFT_CUDA(cudaMemsetAsync(dC, 0, sizeof(float) * static_cast<size_t>(B) * K * D, c.s));
     if (dbias) SOFT_CUDA(cudaMemsetAsync(dbias, 0, sizeof(float) * static_cast<size_t>(B) * K, c.s));
     return KM_OK;
@@ -226,14 +240,11 @@ int km_scores_grad(const void* dS, const uint8_t* xq, const uint8_t* xs, const u
   const int64_t ldd = ceil8(D), ldk = l.copy_ds ? ceil8(K) : K;
   void* cop = c.ws + l.off_cop;
   void* xop = c.ws + l.off_xop;
-  const void* ds = dS;
-  if (l.copy_ds) {
-    void* planes = c.ws + l.off_planes;
-    SOFT_CUDA(launch_split_planes(dS, dtype, static_cast<int64_t>(B) * N, K, ldk, planes, c.s));
-    ds = planes;
-  }
-  if (dX) SOFT_CUDA(launch_dequantize(cq, cs, KM_BF16, static_cast<int64_t>(B) * K, D, ldd, cop, c.s));
-  if (dC) SOFT_CUDA(launch_dequantize(xq, xs, KM_BF16, static_cast<int64_t>(B) * N, D, ldd, xop, c.s));
+  void* planes = l.copy_ds ? c.ws + l.off_planes : nullptr;
+  const void* ds = planes ? planes : dS;
+  const GradPrepArgs pa{cq, cs, dX ? cop : nullptr, static_cast<int64_t>(B) * K, xq, xs, dC ? xop : nullptr,
+                        static_cast<int64_t>(B) * N, D, ldd, dS, dtype, planes, K, ldk, c.status()};
+  SOFT_CUDA(launch_grad_prep(pa, c.s));
   CUtensorMap ds_x, ds_c, cmap, xmap;
   const int64_t depth = static_cast<int64_t>(l.planes) * B;
   if ((r = encode_bf16(&ds_x, ds, K, ldk, N, depth, 256)) != KM_OK) return r;
@@ -309,7 +320,7 @@ int km_balance_grad(const void* S, const uint8_t* valid, const int32_t* counts, 
   if (!aligned16(S) || !aligned16(dS)) return sfail(KM_ERR_INVALID_ARG, "S and dS must be 16-byte aligned");
   int r = check_shape(B, N, 1, K, dtype);
   if (r != KM_OK) return r;
-  if ((r = api_check_device()) != KM_OK) return r;
+  if ((r = check_device_once()) != KM_OK) return r;
   BalanceArgs a{};
   a.S = S;
   a.valid = valid;

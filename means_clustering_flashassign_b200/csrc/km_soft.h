@@ -33,9 +33,8 @@ inline int q_blocks(int D) { return (D + kQBlock - 1) / kQBlock; }
 
 cudaError_t launch_quantize(const void* X, int dtype, int64_t rows, int D, uint8_t* q, uint8_t* scale,
                             cudaStream_t s);
-// Rows of ld_out elements are written (ld_out >= D; columns from D on are left).
-cudaError_t launch_dequantize(const uint8_t* q, const uint8_t* scale, int dtype, int64_t rows, int D, int64_t ld_out,
-                              void* X, cudaStream_t s);
+cudaError_t launch_dequantize(const uint8_t* q, const uint8_t* scale, int dtype, int64_t rows, int D, void* X,
+                              cudaStream_t s);
 
 // ----------------------------------------------------------------- scores
 struct ScoresArgs {
@@ -89,10 +88,31 @@ cudaError_t launch_grad(const GradArgs& a, cudaStream_t s);
 // dC and dbias as the sums of their pieces, in order (nc or nb 0: left out).
 cudaError_t launch_grad_join(const float* cpart, int csplits, int64_t nc, float* dC, const float* bpart, int bsplits,
                              int64_t nb, float* dbias, cudaStream_t s);
-// dS (dtype) as 1 (bf16) or 3 (f32) bf16 planes [planes][rows][ld]; the planes sum to dS
-// exactly for values whose third piece does not underflow.
-cudaError_t launch_split_planes(const void* dS, int dtype, int64_t rows, int K, int64_t ld, void* planes,
-                                cudaStream_t s);
+
+// What launch_grad reads, made from the call's inputs in one launch: the values
+// of the 8-bit operands as bf16 rows of ldd elements, and dS (dtype) as 1
+// (bf16) or 3 (f32) bf16 planes [planes][rows][ldk] which sum to it (exactly,
+// where the third piece does not underflow); clears the status word.  Null
+// outputs are left out; ldd and ldk are multiples of 8.
+struct GradPrepArgs {
+  const uint8_t* cq;
+  const uint8_t* cs;
+  void* cop;
+  int64_t crows;
+  const uint8_t* xq;
+  const uint8_t* xs;
+  void* xop;
+  int64_t xrows;
+  int D;
+  int64_t ldd;
+  const void* dS;
+  int dtype;
+  void* planes;
+  int K;
+  int64_t ldk;
+  unsigned int* status;
+};
+cudaError_t launch_grad_prep(const GradPrepArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------- balance
 struct BalanceArgs {
