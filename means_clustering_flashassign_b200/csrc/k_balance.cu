@@ -65,8 +65,12 @@ struct BalK {
   const float* grad;
 };
 
+// The counts, rows and parts that one kernel of the chain writes are read by the
+// next through L2 (__ldcg): a chained kernel is resident before they are final.
+
 // ------------------------------------------------------------------ counts
 __global__ void __launch_bounds__(kThreads) k_bal_zero(BalK p, int64_t nc, int B) {
+  pdl_wait();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   for (int64_t j = i; j < nc; j += static_cast<int64_t>(gridDim.x) * kThreads) p.counts[j] = 0;
   if (i < B) p.rows[i] = 0, p.done[i] = 0;
@@ -176,7 +180,7 @@ __device__ __forceinline__ void load_shares(const int32_t* counts, int K, int l,
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = (j * LPR + l) * V + i;
-      f[j * V + i] = c < K ? static_cast<float>(counts[c]) * inv : 0.f;
+      f[j * V + i] = c < K ? static_cast<float>(__ldcg(counts + c)) * inv : 0.f;
     }
 }
 
@@ -228,7 +232,7 @@ __device__ __forceinline__ void finish_loss(const BalK& p, int b, int blk, doubl
     for (int i = threadIdx.x; i < p.nblk; i += 32) v += __ldcg(&p.part[static_cast<int64_t>(b) * p.nblk + i]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (threadIdx.x == 0) p.loss[b] = p.rows[b] > 0 ? static_cast<float>(v * p.K / p.rows[b]) : 0.f;
+    if (threadIdx.x == 0) p.loss[b] = __ldcg(&p.rows[b]) > 0 ? static_cast<float>(v * p.K / __ldcg(&p.rows[b])) : 0.f;
   }
 }
 
@@ -250,7 +254,7 @@ __global__ void __launch_bounds__(kThreads) k_bal_rows(const elem_t<BF16>* __res
   const int l = threadIdx.x % LPR;
   pdl_wait();
   float f[E];
-  load_shares<V, LPR, NC, E>(p.counts + static_cast<int64_t>(b) * p.K, p.K, l, share_unit(p.rows[b], p.T), f);
+  load_shares<V, LPR, NC, E>(p.counts + static_cast<int64_t>(b) * p.K, p.K, l, share_unit(__ldcg(&p.rows[b]), p.T), f);
   double sum = 0.0;
   const int64_t step = static_cast<int64_t>(p.nblk) * RPB;
   int64_t i = static_cast<int64_t>(blk) * RPB + threadIdx.x / LPR;
@@ -387,7 +391,7 @@ __global__ void __launch_bounds__(kThreads) k_bal_rows_wide(const elem_t<BF16>* 
   __shared__ float sm[3][kWarps];
   const int b = blockIdx.x / p.nblk, blk = blockIdx.x - b * p.nblk;
   pdl_wait();
-  const float inv = share_unit(p.rows[b], p.T);
+  const float inv = share_unit(__ldcg(&p.rows[b]), p.T);
   const int32_t* cnt = p.counts + static_cast<int64_t>(b) * p.K;
   double sum = 0.0;
   for (int64_t i = blk; i < p.N; i += p.nblk) {
@@ -410,7 +414,7 @@ __global__ void __launch_bounds__(kThreads) k_bal_rows_wide(const elem_t<BF16>* 
           if (j < n) {
             const float e = exp_of(v[j] - sh);
             s += e;
-            t = fmaf(e, static_cast<float>(cnt[c + j]), t);
+            t = fmaf(e, static_cast<float>(__ldcg(cnt + c + j)), t);
           }
       });
     const float top = row_reduce<kThreads, true>(m, sm[0]);
@@ -555,7 +559,6 @@ cudaError_t grad_launch(const BalanceArgs& a, const BalK& k, cudaStream_t s) {
   T* dS = static_cast<T*>(a.dS);
   const unsigned grid = static_cast<unsigned>(k.nblk) * a.B;
   const RowForm r = row_form(a.K, a.dtype);
-  chain_break();
   if (fault_hit(kFaultLaunch)) return cudaErrorLaunchFailure;
   count_launch();
   if (!r.lpr) {
@@ -611,6 +614,7 @@ cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_balance_grad(const BalanceArgs& a, cudaStream_t s) {
+  chain_break();
   if (a.N == 0) return cudaSuccess;
   const BalK k = make_k(a);
   return a.dtype == kDtypeBF16 ? grad_launch<true>(a, k, s) : grad_launch<false>(a, k, s);

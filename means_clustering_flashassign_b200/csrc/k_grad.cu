@@ -424,7 +424,7 @@ template <typename Acc>
 __device__ __forceinline__ Acc join_pieces(const float* part, int pieces, int64_t stride, int64_t i, int ty) {
   Acc v = 0;
 #pragma unroll 4
-  for (int s = ty; s < pieces; s += kJoinY) v += part[static_cast<int64_t>(s) * stride + i];
+  for (int s = ty; s < pieces; s += kJoinY) v += __ldcg(part + static_cast<int64_t>(s) * stride + i);
   return v;
 }
 __global__ void __launch_bounds__(kT) k_grad_join(const float* cpart, int csplits, int64_t nc,
@@ -546,6 +546,7 @@ __device__ __forceinline__ void prep_planes(const float* src, __nv_bfloat16* out
 
 __global__ void __launch_bounds__(kT) k_grad_prep(const __grid_constant__ PrepK p) {
   const GradPrepArgs& a = p.a;
+  pdl_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
   unsigned blk = blockIdx.x;
   if (blk < p.cblocks) {

@@ -215,6 +215,7 @@ unsigned grid_for(int64_t units, int64_t per_block) {
 
 template <bool BF16, bool VEC, int LPB>
 void quantize_t(const void* X, int64_t blocks, int nb, int D, uint8_t* q, uint8_t* scale, cudaStream_t s) {
+  chain_break();
   const unsigned grid = grid_for(blocks, kQThreads / LPB * (BF16 ? 4 : 2));
   const auto* x = static_cast<const elem_t<BF16>*>(X);
   if (blocks < (int64_t(1) << 31))
@@ -225,6 +226,7 @@ void quantize_t(const void* X, int64_t blocks, int nb, int D, uint8_t* q, uint8_
 
 template <bool BF16, bool VEC>
 void quantize_d(const void* X, int64_t blocks, int nb, int D, uint8_t* q, uint8_t* scale, cudaStream_t s) {
+  chain_break();
   // lanes per block: 8 cover 128 coordinates; narrower points need fewer
   if (D > 64) quantize_t<BF16, VEC, 8>(X, blocks, nb, D, q, scale, s);
   else if (D > 32) quantize_t<BF16, VEC, 4>(X, blocks, nb, D, q, scale, s);
@@ -249,8 +251,8 @@ void dequantize_t(const uint8_t* q, const uint8_t* scale, int64_t rows, int D, v
 
 cudaError_t launch_quantize(const void* X, int dtype, int64_t rows, int D, uint8_t* q, uint8_t* scale,
                             cudaStream_t s) {
-  if (rows == 0) return cudaSuccess;
   chain_break();
+  if (rows == 0) return cudaSuccess;
   if (fault_hit(kFaultLaunch)) return cudaErrorLaunchFailure;
   count_launch();
   const int nb = q_blocks(D);
@@ -264,8 +266,8 @@ cudaError_t launch_quantize(const void* X, int dtype, int64_t rows, int D, uint8
 
 cudaError_t launch_dequantize(const uint8_t* q, const uint8_t* scale, int dtype, int64_t rows, int D, void* X,
                               cudaStream_t s) {
-  if (rows == 0) return cudaSuccess;
   chain_break();
+  if (rows == 0) return cudaSuccess;
   if (fault_hit(kFaultLaunch)) return cudaErrorLaunchFailure;
   count_launch();
   const bool vec = D % 8 == 0 && reinterpret_cast<uintptr_t>(X) % 16 == 0;

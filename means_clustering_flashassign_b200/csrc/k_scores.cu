@@ -587,6 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace
 
 cudaError_t launch_scores(const ScoresArgs& a, cudaStream_t s) {
+  chain_break();
   if (a.N == 0) return cudaSuccess;
   ScoresK k{};
   k.xs = a.xs;
@@ -627,7 +628,6 @@ cudaError_t launch_scores(const ScoresArgs& a, cudaStream_t s) {
   auto kern = near ? (bf16 ? k_scores_near<true> : k_scores_near<false>) : (bf16 ? k_scores_wide<true> : k_scores_wide<false>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
   if (e != cudaSuccess) return e;
-  chain_break();
   if (fault_hit(kFaultLaunch)) return cudaErrorLaunchFailure;
   count_launch();
   kern<<<static_cast<unsigned>(grid < nsm ? grid : nsm), kThreads, kSmem, s>>>(*a.xmap, *a.cmap, a.smap ? *a.smap : *a.cmap, k);

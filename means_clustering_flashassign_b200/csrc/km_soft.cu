@@ -203,6 +203,7 @@ int km_scores(const uint8_t* xq, const uint8_t* xs, const uint8_t* cq, const uin
   int r = soft_prepare(c, KM_SOFT_SCORES, B, N, D, K, dtype, workspace, workspace_bytes, stream);
   if (r != KM_OK) return r;
   SOFT_CUDA(cudaMemsetAsync(c.status(), 0, sizeof(unsigned int), c.s));
+  chain_break();
   if (N == 0) return KM_OK;
   CUtensorMap xmap, cmap, smap;
   if ((r = encode_q(&xmap, xq, D, N, B)) != KM_OK) return r;
@@ -235,6 +236,7 @@ int km_scores_grad(const void* dS, const uint8_t* xq, const uint8_t* xs, const u
     SOFT_CUDA(cudaMemsetAsync(c.status(), 0, sizeof(unsigned int), c.s));
     if (dC) SOFT_CUDA(cudaMemsetAsync(dC, 0, sizeof(float) * static_cast<size_t>(B) * K * D, c.s));
     if (dbias) SOFT_CUDA(cudaMemsetAsync(dbias, 0, sizeof(float) * static_cast<size_t>(B) * K, c.s));
+    chain_break();
     return KM_OK;
   }
   const int64_t ldd = ceil8(D), ldk = l.copy_ds ? ceil8(K) : K;

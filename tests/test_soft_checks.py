@@ -154,3 +154,17 @@ def test_valid_calls_without_a_gpu_report_the_device():
     p = ctypes.c_void_p((ctypes.addressof(buf) + 255) // 256 * 256)
     assert L.km_quantize(p, 1, 4, 8, km.F32, p, p, None) == 3
     assert L.km_scores(p, p, p, p, None, 1.0, 1, 4, 8, 4, km.F32, p, p, 4096, None) == 3
+
+
+@pytest.mark.parametrize("kernel", ["k_grad_prep", "k_grad", "k_grad_join", "k_bal_zero", "k_bal_count", "k_bal_rows",
+                                    "k_bal_rows_wide"])
+def test_chained_kernels_wait_before_they_touch_the_chains_data(kernel):
+    """The same rule as for the kernels of a Lloyd iteration: every kernel that
+    may be launched with programmatic stream serialization waits on the device
+    before it can return."""
+    import test_chain_rule as rule
+    bodies = rule._kernel_bodies(kernel)
+    assert bodies
+    for fname, body in bodies:
+        w = body.find("pdl_wait();")
+        assert w >= 0 and "return;" not in body[:w], (kernel, fname)
