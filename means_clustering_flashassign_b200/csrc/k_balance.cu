@@ -34,6 +34,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kHistMax = 8192;  // clusters a block counts in shared memory
+constexpr int kSolo = 1024;     // threads of the block that counts a small instance alone
 constexpr int kRegCols = 32;    // columns of a row per thread, at most
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -80,22 +81,23 @@ __global__ void __launch_bounds__(kThreads) k_bal_zero(BalK p, int64_t nc, int B
 // instance take its points round robin; one block alone (SOLO) writes its
 // histogram without adding, so that nothing has to be zeroed before.
 template <bool SOLO>
-__global__ void __launch_bounds__(kThreads) k_bal_count(BalK p, int nblk) {
+__global__ void __launch_bounds__(SOLO ? kSolo : kThreads) k_bal_count(BalK p, int nblk) {
+  constexpr int kN = SOLO ? kSolo : kThreads;
   extern __shared__ int32_t hist[];
   __shared__ int32_t valid_rows;
   const int b = blockIdx.x / nblk, blk = blockIdx.x - b * nblk;
   const bool local = SOLO || p.K <= kHistMax;
   if (threadIdx.x == 0) valid_rows = 0;
   if (local)
-    for (int k = threadIdx.x; k < p.K; k += kThreads) hist[k] = 0;
+    for (int k = threadIdx.x; k < p.K; k += kN) hist[k] = 0;
   __syncthreads();
   pdl_wait();
   const int32_t* idx = p.idx + b * p.N * p.T;
   const uint8_t* valid = p.valid ? p.valid + b * p.N : nullptr;
   int32_t* counts = p.counts + static_cast<int64_t>(b) * p.K;
   int n = 0;
-  for (int64_t i = static_cast<int64_t>(blk) * kThreads + threadIdx.x; i < p.N;
-       i += static_cast<int64_t>(nblk) * kThreads) {
+  for (int64_t i = static_cast<int64_t>(blk) * kN + threadIdx.x; i < p.N;
+       i += static_cast<int64_t>(nblk) * kN) {
     if (valid && !valid[i]) continue;
     ++n;
     for (int t = 0; t < p.T; ++t) {
@@ -108,11 +110,11 @@ __global__ void __launch_bounds__(kThreads) k_bal_count(BalK p, int nblk) {
   if ((threadIdx.x & 31) == 0 && n) atomicAdd(&valid_rows, n);
   __syncthreads();
   if (SOLO) {
-    for (int k = threadIdx.x; k < p.K; k += kThreads) counts[k] = hist[k];
+    for (int k = threadIdx.x; k < p.K; k += kN) counts[k] = hist[k];
     if (threadIdx.x == 0) p.rows[b] = valid_rows, p.done[b] = 0;
   } else {
     if (local)
-      for (int k = threadIdx.x; k < p.K; k += kThreads)
+      for (int k = threadIdx.x; k < p.K; k += kN)
         if (hist[k]) atomicAdd(&counts[k], hist[k]);
     if (threadIdx.x == 0 && valid_rows) atomicAdd(&p.rows[b], valid_rows);
   }
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(kThreads) k_bal_rows(const elem_t<BF16>* __res
 }
 
 template <bool BF16, bool VEC, int LPR, int NC>
-__global__ void __launch_bounds__(kThreads, 3) k_bal_grad(const elem_t<BF16>* __restrict__ S,
+__global__ void __launch_bounds__(kThreads, 2) k_bal_grad(const elem_t<BF16>* __restrict__ S,
                                                        elem_t<BF16>* __restrict__ dS, const BalK p) {
   constexpr int V = VEC ? (BF16 ? 8 : 4) : 1, E = NC * V, RPB = kThreads / LPR;
   const int b = blockIdx.x / p.nblk, blk = blockIdx.x - b * p.nblk;
@@ -305,20 +307,31 @@ __global__ void __launch_bounds__(kThreads, 3) k_bal_grad(const elem_t<BF16>* __
   load_shares<V, LPR, NC, E>(p.counts + static_cast<int64_t>(b) * p.K, p.K, l, share_unit(M, p.T), f);
 #pragma unroll
   for (int j = 0; j < E; ++j) f[j] *= coef;
-  Raw<BF16, VEC, NC> raw;
+  Raw<BF16, VEC, NC> next;
   const int64_t step = static_cast<int64_t>(p.nblk) * RPB;
-  for (int64_t i = static_cast<int64_t>(blk) * RPB + threadIdx.x / LPR; i < p.N; i += step) {
+  int64_t i = static_cast<int64_t>(blk) * RPB + threadIdx.x / LPR;
+  float ls = 0.f, r = 0.f;
+  bool on = false;
+  // the row's numbers and, where it has probabilities, its scores
+  auto fetch = [&](int64_t row) {
+    if (row >= p.N) return;
+    const int64_t o = b * p.N + row;
+    ls = p.lse[o], r = p.dot[o];
+    on = (!p.valid || p.valid[o]) && ls != -CUDART_INF_F;
+    load_raw<BF16, VEC, LPR, NC>(next, S + o * p.K, p.K, l, on);
+  };
+  fetch(i);
+  for (; i < p.N; i += step) {
     const int64_t o = b * p.N + i;
-    const float ls = p.lse[o], r = p.dot[o];
-    const bool on = (!p.valid || p.valid[o]) && ls != -CUDART_INF_F;
     float x[E];
     if (on) {
-      load_raw<BF16, VEC, LPR, NC>(raw, S + o * p.K, p.K, l, true);
-      unpack_raw<BF16, VEC, NC, E>(raw, x);
-      const float rc = r * coef;
+      unpack_raw<BF16, VEC, NC, E>(next, x);
+      const float rc = r * coef, l0 = ls;
+      fetch(i + step);
 #pragma unroll
-      for (int j = 0; j < E; ++j) x[j] = exp_of(x[j] - ls) * (f[j] - rc);
+      for (int j = 0; j < E; ++j) x[j] = exp_of(x[j] - l0) * (f[j] - rc);
     } else {
+      fetch(i + step);
 #pragma unroll
       for (int j = 0; j < E; ++j) x[j] = 0.f;
     }
@@ -593,7 +606,7 @@ cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t s) {
   const size_t sm = a.K <= kHistMax ? sizeof(int32_t) * a.K : 0;
   if (solo) {
     count_launch();
-    e = launch_chained(k_bal_count<true>, dim3(a.B), dim3(kThreads), sm, s, k, 1);
+    e = launch_chained(k_bal_count<true>, dim3(a.B), dim3(kSolo), sm, s, k, 1);
   } else {
     const int64_t nc = static_cast<int64_t>(a.B) * a.K;
     const int64_t zb = (nc + kThreads - 1) / kThreads, mb = (a.B + kThreads - 1) / kThreads;

@@ -98,6 +98,26 @@ __device__ __forceinline__ void add_bf16x2(float& s0, float& s1, uint32_t w) {
       : "r"(w));
 }
 
+// L2 policies: a dS line is read twice, and the second time is the last.
+__device__ __forceinline__ uint64_t policy_keep() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint64_t policy_drop() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar)), "l"(policy)
+      : "memory");
+}
+
 // KT centroids per dC tile (the MMA's N).
 template <int KT, bool OUT_BF16, bool WX, bool WC, bool WB>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -156,6 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       prefetch_tensormap(&ds_c);
       prefetch_tensormap(&cmap);
       prefetch_tensormap(&xmap);
+      const uint64_t keep = policy_keep(), drop = policy_drop();
       int st = 0;
       uint32_t ph = 0;
       int issued[kStages];
@@ -178,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive_expect_tx(&full[st], kStageB);
                 tma_load_3d(dst, &cmap, d0, l * kSlice, w.b, &full[st]);
                 tma_load_3d(dst + kBoxBytes, &cmap, d0 + 64, l * kSlice, w.b, &full[st]);
-                tma_load_3d(dst + kABytes, &ds_x, l * kSlice, r0, pl * p.B + w.b, &full[st]);
+                tma_load_3d_hint(dst + kABytes, &ds_x, l * kSlice, r0, pl * p.B + w.b, &full[st], keep);
                 issued[st] = static_cast<int>(ph);
                 next();
               }
@@ -195,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_3d(dst + kBoxBytes, &xmap, d0 + 64, r0, w.b, &full[st]);
 #pragma unroll
                 for (int j = 0; j < KT / 64; ++j)
-                  tma_load_3d(dst + kABytes + j * kBoxBytes, &ds_c, kt * KT + j * 64, r0, pl * p.B + w.b, &full[st]);
+                  tma_load_3d_hint(dst + kABytes + j * kBoxBytes, &ds_c, kt * KT + j * 64, r0, pl * p.B + w.b, &full[st], drop);
                 issued[st] = static_cast<int>(ph);
                 next();
               }
@@ -361,8 +382,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           held = 0;
         };
         for (int64_t t = w.t0; ok && t < w.t1; t += p.group) {
+          // dX's slices are not looked at, but waited for: a barrier's parity tells
+          // only neighbouring phases apart, so no role may skip a stage's turn
           const int nx = WX && ps == 0 && t + me < w.t1 ? kslices * p.planes : 0;
-          for (int i = 0; i < nx; ++i) {  // dX's slices: not looked at
+          for (int i = 0; i < nx; ++i) {
             if (!__all_sync(0xffffffffu, mbar_wait(&full[st], ph, g))) { ok = false; break; }
             if (lane == 0) mbar_arrive(&empty[st]);
             next();
@@ -416,34 +439,34 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------ small kernels
 constexpr int kT = 256;
 
-// out[i] = sum over the pieces, for dC (nc elements) and dbias (nb): 32 outputs
-// per block, 8 threads for each, every thread's pieces in order and then the 8
-// in order (the pieces of a small problem are many and its outputs few).
-constexpr int kJoinX = 32, kJoinY = 8;
-template <typename Acc>
+// out[i] = sum over the pieces, for dC (nc elements) and dbias (nb): Y threads for
+// each output, every thread's pieces in order and then the Y in order (the
+// pieces of a small problem are many and its outputs few).
+template <typename Acc, int Y>
 __device__ __forceinline__ Acc join_pieces(const float* part, int pieces, int64_t stride, int64_t i, int ty) {
   Acc v = 0;
-#pragma unroll 4
-  for (int s = ty; s < pieces; s += kJoinY) v += __ldcg(part + static_cast<int64_t>(s) * stride + i);
+#pragma unroll 8
+  for (int s = ty; s < pieces; s += Y) v += __ldcg(part + static_cast<int64_t>(s) * stride + i);
   return v;
 }
-__global__ void __launch_bounds__(kT) k_grad_join(const float* cpart, int csplits, int64_t nc,
-                                                  float* __restrict__ dC, const float* bpart, int bsplits,
-                                                  int64_t nb, float* __restrict__ dbias) {
-  __shared__ double sum[kJoinY][kJoinX];
-  const int tx = threadIdx.x % kJoinX, ty = threadIdx.x / kJoinX;
+template <int Y>
+__global__ void __launch_bounds__(kT) k_grad_join(const float* cpart, int csplits, int64_t nc, float* __restrict__ dC,
+                                                  const float* bpart, int bsplits, int64_t nb,
+                                                  float* __restrict__ dbias) {
+  constexpr int X = kT / Y;
+  __shared__ double sum[Y][X];
+  const int tx = threadIdx.x % X, ty = threadIdx.x / X;
   pdl_wait();
-  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kJoinX; i0 < nc + nb;
-       i0 += static_cast<int64_t>(gridDim.x) * kJoinX) {
+  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * X; i0 < nc + nb; i0 += static_cast<int64_t>(gridDim.x) * X) {
     const int64_t i = i0 + tx;
     double v = 0.0;
-    if (i < nc) v = join_pieces<float>(cpart, csplits, nc, i, ty);
-    else if (i < nc + nb) v = join_pieces<double>(bpart, bsplits, nb, i - nc, ty);
+    if (i < nc) v = join_pieces<float, Y>(cpart, csplits, nc, i, ty);
+    else if (i < nc + nb) v = join_pieces<double, Y>(bpart, bsplits, nb, i - nc, ty);
     sum[ty][tx] = v;
     __syncthreads();
     if (ty == 0 && i < nc + nb) {
 #pragma unroll
-      for (int j = 1; j < kJoinY; ++j) v += sum[j][tx];
+      for (int j = 1; j < Y; ++j) v += sum[j][tx];
       if (i < nc) dC[i] = static_cast<float>(v);
       else dbias[i - nc] = static_cast<float>(v);
     }
@@ -659,7 +682,11 @@ cudaError_t launch_grad(const GradArgs& a, cudaStream_t s) {
 cudaError_t launch_grad_join(const float* cpart, int csplits, int64_t nc, float* dC, const float* bpart, int bsplits,
                              int64_t nb, float* dbias, cudaStream_t s) {
   count_launch();
-  return launch_chained(k_grad_join, dim3(grid_of((nc + nb) * kJoinY)), dim3(kT), 0, s, cpart, csplits, nc, dC, bpart,
+  // 8 threads per output fill the device from 38K outputs on; below that, 32
+  if ((nc + nb) * 8 >= 148 * 8 * kT)
+    return launch_chained(k_grad_join<8>, dim3(grid_of((nc + nb) * 8)), dim3(kT), 0, s, cpart, csplits, nc, dC, bpart,
+                          bsplits, nb, dbias);
+  return launch_chained(k_grad_join<32>, dim3(grid_of((nc + nb) * 32)), dim3(kT), 0, s, cpart, csplits, nc, dC, bpart,
                         bsplits, nb, dbias);
 }
 
