@@ -38,6 +38,10 @@ constexpr int kSolo = 1024;     // threads of the block that counts a small inst
 constexpr int kRegCols = 32;    // columns of a row per thread, at most
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Blocks of the row kernels an SM holds at once (their registers are bounded for
+// it).
+__host__ __device__ constexpr int resident(bool vec, int nc) { return vec ? 3 : (nc <= 4 ? 5 : (nc == 8 ? 4 : 2)); }
+
 template <bool BF16>
 using elem_t = typename std::conditional<BF16, __nv_bfloat16, float>::type;
 
@@ -150,40 +154,78 @@ __device__ __forceinline__ void load_raw(Raw<BF16, VEC, NC>& r, const elem_t<BF1
   }
 }
 
-template <bool BF16, bool VEC, int NC, int E>
-__device__ __forceinline__ void unpack_raw(const Raw<BF16, VEC, NC>& r, float (&x)[E]) {
-  constexpr int V = VEC ? (BF16 ? 8 : 4) : 1;
+// The values of chunk j.  Kernels keep the raw words and take the values a chunk at
+// a time: half the registers for bf16, and a third block per SM for it.
+template <bool BF16, bool VEC, int NC, int V>
+__device__ __forceinline__ void chunk_of(const Raw<BF16, VEC, NC>& r, int j, float (&x)[V]) {
+  if constexpr (VEC) {
+    const uint32_t w[4] = {r.w[j].x, r.w[j].y, r.w[j].z, r.w[j].w};
 #pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    if constexpr (VEC) {
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (BF16) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      } else {
+        x[i] = __uint_as_float(w[i]);
+      }
+    }
+  } else if constexpr (BF16) {
+    x[0] = __uint_as_float(static_cast<uint32_t>(r.w[j]) << 16);
+  } else {
+    x[0] = __uint_as_float(r.w[j]);
+  }
+}
+
+// The largest value (a NaN only if there is nothing else).
+template <bool BF16, bool VEC, int NC>
+__device__ __forceinline__ float max_of(const Raw<BF16, VEC, NC>& r) {
+  if constexpr (VEC && BF16) {  // two at a time
+    uint32_t m = 0xff80ff80u;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
       const uint32_t w[4] = {r.w[j].x, r.w[j].y, r.w[j].z, r.w[j].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (BF16) {
-          x[j * V + 2 * i] = __uint_as_float(w[i] << 16);
-          x[j * V + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        } else {
-          x[j * V + i] = __uint_as_float(w[i]);
-        }
-      }
-    } else if constexpr (BF16) {
-      x[j] = __uint_as_float(static_cast<uint32_t>(r.w[j]) << 16);
-    } else {
-      x[j] = __uint_as_float(r.w[j]);
+      for (int i = 0; i < 4; ++i) asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
     }
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  } else {
+    constexpr int V = VEC ? 4 : 1;
+    float m = -CUDART_INF_F;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      float x[V];
+      chunk_of<BF16, VEC, NC, V>(r, j, x);
+#pragma unroll
+      for (int i = 0; i < V; ++i) m = fmaxf(m, x[i]);
+    }
+    return m;
   }
 }
 
 // The shares of this thread's columns.
 template <int V, int LPR, int NC, int E>
 __device__ __forceinline__ void load_shares(const int32_t* counts, int K, int l, float inv, float (&f)[E]) {
+  const bool wide = V % 4 == 0 && reinterpret_cast<uintptr_t>(counts) % 16 == 0;
 #pragma unroll
-  for (int j = 0; j < NC; ++j)
+  for (int j = 0; j < NC; ++j) {
+    const int c0 = (j * LPR + l) * V;
+    if (wide) {  // K is a multiple of V
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (j * LPR + l) * V + i;
-      f[j * V + i] = c < K ? static_cast<float>(__ldcg(counts + c)) * inv : 0.f;
+      for (int i = 0; i < V; i += 4) {
+        const int4 n = c0 < K ? __ldcg(reinterpret_cast<const int4*>(counts + c0 + i)) : make_int4(0, 0, 0, 0);
+        f[j * V + i] = static_cast<float>(n.x) * inv;
+        if constexpr (V >= 4) {
+          f[j * V + i + 1] = static_cast<float>(n.y) * inv;
+          f[j * V + i + 2] = static_cast<float>(n.z) * inv;
+          f[j * V + i + 3] = static_cast<float>(n.w) * inv;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        f[j * V + i] = c0 + i < K ? static_cast<float>(__ldcg(counts + c0 + i)) * inv : 0.f;
     }
+  }
 }
 
 __device__ __forceinline__ float share_unit(int64_t M, int T) {
@@ -194,10 +236,14 @@ __device__ __forceinline__ float share_unit(int64_t M, int T) {
 // memory, where every thread of the block takes part.
 template <int LPR, bool MAX>
 __device__ __forceinline__ float row_reduce(float v, float* sm) {
+  if constexpr (LPR >= 32 && MAX) {
+    asm volatile("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(v));
+  } else {
 #pragma unroll
   for (int o = (LPR < 32 ? LPR : 32) / 2; o > 0; o >>= 1) {
     const float u = __shfl_xor_sync(0xffffffffu, v, o);
     v = MAX ? fmaxf(v, u) : v + u;
+  }
   }
   if constexpr (LPR > 32) {
     constexpr int W = LPR / 32;
@@ -249,7 +295,7 @@ __device__ __forceinline__ RowNumbers row_numbers(float m, float s, float t) {
 }
 
 template <bool BF16, bool VEC, int LPR, int NC>
-__global__ void __launch_bounds__(kThreads) k_bal_rows(const elem_t<BF16>* __restrict__ S, const BalK p) {
+__global__ void __launch_bounds__(kThreads, resident(VEC, NC)) k_bal_rows(const elem_t<BF16>* __restrict__ S, const BalK p) {
   constexpr int V = VEC ? (BF16 ? 8 : 4) : 1, E = NC * V, RPB = kThreads / LPR;
   __shared__ float sm[3][kWarps];
   const int b = blockIdx.x / p.nblk, blk = blockIdx.x - b * p.nblk;
@@ -266,22 +312,23 @@ __global__ void __launch_bounds__(kThreads) k_bal_rows(const elem_t<BF16>* __res
   load_raw<BF16, VEC, LPR, NC>(next, S + (b * p.N + i) * p.K, p.K, l, on);
   // every thread of the block runs the same rounds (the reductions may span it)
   for (int64_t base = static_cast<int64_t>(blk) * RPB; base < p.N; base += step, i += step) {
-    float x[E];
-    unpack_raw<BF16, VEC, NC, E>(next, x);
+    const Raw<BF16, VEC, NC> raw = next;
     const bool now = on;
     on = usable(i + step);
     load_raw<BF16, VEC, LPR, NC>(next, S + (b * p.N + i + step) * p.K, p.K, l, on);
-    float m = x[0];
-#pragma unroll
-    for (int j = 1; j < E; ++j) m = fmaxf(m, x[j]);
-    m = row_reduce<LPR, true>(m, sm[0]);
+    const float m = row_reduce<LPR, true>(max_of<BF16, VEC, NC>(raw), sm[0]);
     const float sh = m == -CUDART_INF_F ? 0.f : m;
     float s = 0.f, t = 0.f;
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const float e = exp_of(x[j] - sh);
-      s += e;
-      t = fmaf(e, f[j], t);
+    for (int j = 0; j < NC; ++j) {
+      float x[V];
+      chunk_of<BF16, VEC, NC, V>(raw, j, x);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float e = exp_of(x[i] - sh);
+        s += e;
+        t = fmaf(e, f[j * V + i], t);
+      }
     }
     s = row_reduce<LPR, false>(s, sm[1]);
     t = row_reduce<LPR, false>(t, sm[2]);
@@ -296,7 +343,7 @@ __global__ void __launch_bounds__(kThreads) k_bal_rows(const elem_t<BF16>* __res
 }
 
 template <bool BF16, bool VEC, int LPR, int NC>
-__global__ void __launch_bounds__(kThreads, 2) k_bal_grad(const elem_t<BF16>* __restrict__ S,
+__global__ void __launch_bounds__(kThreads, resident(VEC, NC)) k_bal_grad(const elem_t<BF16>* __restrict__ S,
                                                        elem_t<BF16>* __restrict__ dS, const BalK p) {
   constexpr int V = VEC ? (BF16 ? 8 : 4) : 1, E = NC * V, RPB = kThreads / LPR;
   const int b = blockIdx.x / p.nblk, blk = blockIdx.x - b * p.nblk;
@@ -322,38 +369,33 @@ __global__ void __launch_bounds__(kThreads, 2) k_bal_grad(const elem_t<BF16>* __
   };
   fetch(i);
   for (; i < p.N; i += step) {
-    const int64_t o = b * p.N + i;
-    float x[E];
-    if (on) {
-      unpack_raw<BF16, VEC, NC, E>(next, x);
-      const float rc = r * coef, l0 = ls;
-      fetch(i + step);
-#pragma unroll
-      for (int j = 0; j < E; ++j) x[j] = exp_of(x[j] - l0) * (f[j] - rc);
-    } else {
-      fetch(i + step);
-#pragma unroll
-      for (int j = 0; j < E; ++j) x[j] = 0.f;
-    }
-    elem_t<BF16>* out = dS + o * p.K;
+    const Raw<BF16, VEC, NC> raw = next;
+    const float rc = r * coef, l0 = ls;
+    const bool now = on;
+    elem_t<BF16>* out = dS + (b * p.N + i) * p.K;
+    fetch(i + step);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int c = (j * LPR + l) * V;
       if (c >= p.K) continue;
+      float x[V];
+      chunk_of<BF16, VEC, NC, V>(raw, j, x);
+#pragma unroll
+      for (int k = 0; k < V; ++k) x[k] = now ? exp_of(x[k] - l0) * (f[j * V + k] - rc) : 0.f;
       if constexpr (VEC && BF16) {
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(x[j * V + 2 * k], x[j * V + 2 * k + 1]);
+          const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
           w[k] = *reinterpret_cast<const uint32_t*>(&h);
         }
         __stcs(reinterpret_cast<uint4*>(out + c), make_uint4(w[0], w[1], w[2], w[3]));
       } else if constexpr (VEC) {
-        __stcs(reinterpret_cast<float4*>(out + c), make_float4(x[j * V], x[j * V + 1], x[j * V + 2], x[j * V + 3]));
+        __stcs(reinterpret_cast<float4*>(out + c), make_float4(x[0], x[1], x[2], x[3]));
       } else if constexpr (BF16) {
-        out[c] = __float2bfloat16_rn(x[j]);
+        out[c] = __float2bfloat16_rn(x[0]);
       } else {
-        out[c] = x[j];
+        out[c] = x[0];
       }
     }
   }
@@ -508,25 +550,17 @@ RowForm row_form(int K, int dtype) {
   if (r.lpr > kThreads) r.lpr = 0;
   return r;
 }
-int rows_per_block(int K, int dtype) {
-  const RowForm r = row_form(K, dtype);
-  return r.lpr ? kThreads / r.lpr : 1;
-}
-
-// Calls go(LPR, NC) with the form's compile-time sizes.
+// Calls go(VEC, LPR, NC) with the form's compile-time values.
 template <typename Go>
 void with_form(const RowForm& r, Go&& go) {
-  auto c = [](auto x) { return x; };
   using std::integral_constant;
-#define KM_CASE(L, N) \
-  if (r.lpr == L && r.nc == N) return go(c(integral_constant<int, L>{}), c(integral_constant<int, N>{}));
-  if (r.vec) {
-    KM_CASE(1, 4) KM_CASE(2, 4) KM_CASE(4, 4) KM_CASE(8, 4) KM_CASE(16, 4) KM_CASE(32, 4) KM_CASE(64, 4)
-    KM_CASE(128, 4) KM_CASE(256, 4)
-  } else {
-    KM_CASE(32, 1) KM_CASE(32, 2) KM_CASE(32, 4) KM_CASE(32, 8) KM_CASE(32, 16) KM_CASE(32, 32) KM_CASE(64, 32)
-    KM_CASE(128, 32) KM_CASE(256, 32)
-  }
+#define KM_CASE(VEC, L, N)                    \
+  if (r.vec == VEC && r.lpr == L && r.nc == N) \
+    return go(integral_constant<bool, VEC>{}, integral_constant<int, L>{}, integral_constant<int, N>{});
+  KM_CASE(true, 1, 4) KM_CASE(true, 2, 4) KM_CASE(true, 4, 4) KM_CASE(true, 8, 4) KM_CASE(true, 16, 4)
+  KM_CASE(true, 32, 4) KM_CASE(true, 64, 4) KM_CASE(true, 128, 4) KM_CASE(true, 256, 4)
+  KM_CASE(false, 32, 1) KM_CASE(false, 32, 2) KM_CASE(false, 32, 4) KM_CASE(false, 32, 8) KM_CASE(false, 32, 16)
+  KM_CASE(false, 32, 32) KM_CASE(false, 64, 32) KM_CASE(false, 128, 32) KM_CASE(false, 256, 32)
 #undef KM_CASE
 }
 
@@ -558,9 +592,8 @@ cudaError_t rows_launch(const BalanceArgs& a, const BalK& k, cudaStream_t s) {
   cudaError_t e = cudaErrorInvalidValue;
   count_launch();
   if (!r.lpr) return launch_chained(k_bal_rows_wide<BF16>, grid, dim3(kThreads), 0, s, S, k);
-  with_form(r, [&](auto L, auto N) {
-    e = r.vec ? launch_chained(k_bal_rows<BF16, true, L(), (N() > 4 ? 4 : N())>, grid, dim3(kThreads), 0, s, S, k)
-              : launch_chained(k_bal_rows<BF16, false, (L() < 32 ? 32 : L()), N()>, grid, dim3(kThreads), 0, s, S, k);
+  with_form(r, [&](auto V, auto L, auto N) {
+    e = launch_chained(k_bal_rows<BF16, V(), L(), N()>, grid, dim3(kThreads), 0, s, S, k);
   });
   return e;
 }
@@ -577,25 +610,26 @@ cudaError_t grad_launch(const BalanceArgs& a, const BalK& k, cudaStream_t s) {
   if (!r.lpr) {
     k_bal_grad_wide<BF16><<<grid, kThreads, 0, s>>>(S, dS, k);
   } else {
-    with_form(r, [&](auto L, auto N) {
-      if (r.vec) k_bal_grad<BF16, true, L(), (N() > 4 ? 4 : N())><<<grid, kThreads, 0, s>>>(S, dS, k);
-      else k_bal_grad<BF16, false, (L() < 32 ? 32 : L()), N()><<<grid, kThreads, 0, s>>>(S, dS, k);
-    });
+    with_form(r, [&](auto V, auto L, auto N) { k_bal_grad<BF16, V(), L(), N()><<<grid, kThreads, 0, s>>>(S, dS, k); });
   }
   return cudaGetLastError();
 }
 
 }  // namespace
 
-// Blocks per instance of the row passes: the device a few times over, at least
-// two rounds of rows each.
-int balance_blocks(int B, int64_t N, int K, int dtype) {
-  const int rpb = rows_per_block(K, dtype);
-  int64_t n = (148 * 8 + B - 1) / B;
+// Blocks per instance of the row passes, each with two rounds of rows at least:
+// eight per SM in the forward pass, whose blocks then even out what the SMs'
+// distance from the memory makes uneven (418 against 460 us for one wave, 1M x
+// 1024 bf16), and one wave of them in the gradient, which stores as much as it
+// loads (698 against 736 us for eight per SM).
+static int blocks_for(int B, int64_t N, const RowForm& r, int per_sm) {
+  const int rpb = r.lpr ? kThreads / r.lpr : 1;
+  int64_t n = (148 * per_sm + B - 1) / B;
   const int64_t most = (N + 2 * rpb - 1) / (2 * rpb);
   if (n > most) n = most;
   return static_cast<int>(n < 1 ? 1 : n);
 }
+int balance_blocks(int B, int64_t N, int K, int dtype) { return blocks_for(B, N, row_form(K, dtype), 8); }
 
 cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t s) {
   const BalK k = make_k(a);
@@ -629,7 +663,9 @@ cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t s) {
 cudaError_t launch_balance_grad(const BalanceArgs& a, cudaStream_t s) {
   chain_break();
   if (a.N == 0) return cudaSuccess;
-  const BalK k = make_k(a);
+  BalK k = make_k(a);
+  const RowForm r = row_form(a.K, a.dtype);
+  k.nblk = blocks_for(a.B, a.N, r, r.lpr ? resident(r.vec, r.nc) : 8);
   return a.dtype == kDtypeBF16 ? grad_launch<true>(a, k, s) : grad_launch<false>(a, k, s);
 }
 
