@@ -23,9 +23,11 @@
 // Both accumulators (256 columns each) stay in tensor memory side by side, so
 // that dX's epilogue runs under dC's MMAs.
 //
-// Structure: warp 0 TMA, warp 1 MMA, warps 2..9 epilogue, warps 10..17 column
+// Structure: warp 0 TMA, warp 1 MMA, warps 4..11 epilogue, warps 12..15 column
 // sums (dbias, from the staged dS slices of the dC product: float32 over 16
-// points, those joined in float64).  Every wait is bounded in time.
+// points, those joined in float64).  The epilogue warps hold a whole dC tile in
+// registers, 128 sums a thread, so the warpgroups divide the launch's registers
+// anew (setmaxnreg).  Every wait is bounded in time.
 #include "km_e4m3.cuh"
 #include "km_internal.h"
 #include "km_soft.h"
@@ -35,7 +37,7 @@ namespace km {
 
 namespace {
 
-constexpr int kThreads = 576;
+constexpr int kThreads = 512;  // four warpgroups
 constexpr int kDT = 128;       // coordinates per tile (MMA M)
 constexpr int kRT = 256;       // points per dX tile (MMA N)
 constexpr int kSlice = 64;     // terms of a sum per stage
@@ -44,7 +46,14 @@ constexpr int kBBytes = kRT * kSlice * 2;
 constexpr int kBoxBytes = kSlice * 64 * 2;  // 64 terms x 64 columns
 constexpr int kStageB = kABytes + kBBytes;
 constexpr int kStages = 4;
-constexpr int kEpiWarps = 8, kSumWarps = 8;
+constexpr int kEpiWarps = 8, kSumWarps = 4;
+constexpr int kEpiWarp0 = 4, kSumWarp0 = kEpiWarp0 + kEpiWarps;
+// Slices of one accumulation, at most: dC's are added up in registers, dX's
+// (float32) in memory.
+constexpr int kChainC = 8, kChainX = 16;
+// Registers per thread: at launch, and as the warpgroups divide them.
+constexpr int kRegsLaunch = 128, kRegsEpi = 184, kRegsRest = 72;
+static_assert(32 * kEpiWarps * kRegsEpi + (kThreads - 32 * kEpiWarps) * kRegsRest <= kThreads * kRegsLaunch, "registers");
 constexpr uint32_t kTmemCols = 512;
 constexpr size_t kSmem = 1024 + kStages * kStageB + 32 * 8;
 
@@ -89,6 +98,107 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
   d |= static_cast<uint64_t>(1u) << 46;
   d |= static_cast<uint64_t>(2u) << 61;
   return d;
+}
+
+// Every slice of a CTA's walk in order, the same in every role: per item and pass,
+// per step, the nx centroid slices of this CTA's own dX tile (x) and the nc point
+// slices of the group's step.
+//
+// The tensor core truncates where it adds to its float32 accumulator, so a
+// chain of n MMAs loses up to n 2^-24 of its size, always toward zero: 443 of
+// them (dC of 1M points in 37 pieces) left 8e-5 of the result, 32 leave less
+// than 1e-6.  So dC's chains end after kChainC slices (four MMAs each), and
+// their sums are added in registers, rounded to nearest.  The dX slices are
+// dealt out between them: each chain is read from tensor memory while the MMAs
+// go on with dX.  A float32 dX's chains of kChainX are added in memory (one
+// thread adds to an element, in order: the result is reproducible); a bf16 dX
+// takes its K terms in one.
+template <bool WX, bool ROWS, bool XCHAINS>
+struct Cursor {
+  const GradK& p;
+  const int64_t step;    // groups
+  const int me;
+  int64_t item, t;
+  Walk w;
+  int ps = 0, kt;
+  int nx, nc, parts;     // of the step: slices, and how often the two alternate
+  int part, i, e;        // this slice, and where its run of slices ends
+  bool x, live = true;
+  __device__ __forceinline__ Cursor(const GradK& p_, int64_t grp, int me_)
+      : p(p_), step(p_.groups), me(me_), item(grp), w(grp, p_), kt(me_) {
+    if (item >= p.items) { live = false; return; }
+    t = w.t0;
+    open();
+    if (i == e) advance();
+  }
+  __device__ __forceinline__ void open() {
+    nx = WX && ps == 0 && t + me < w.t1 ? (p.K + kSlice - 1) / kSlice * p.planes : 0;
+    const int64_t r0 = t * kRT, end = (t + p.group < w.t1 ? t + p.group : w.t1) * kRT;
+    nc = ROWS && kt < p.nkt ? static_cast<int>(((end < p.N ? end : p.N) - r0 + kSlice - 1) / kSlice) * p.planes : 0;
+    parts = nc > kChainC ? (nc + kChainC - 1) / kChainC : 1;
+    part = 0;
+    x = true;
+    run();
+  }
+  __device__ __forceinline__ void run() {
+    if (x) {
+      i = static_cast<int>(static_cast<int64_t>(part) * nx / parts);
+      e = static_cast<int>(static_cast<int64_t>(part + 1) * nx / parts);
+    } else {
+      i = part * kChainC;
+      e = i + kChainC < nc ? i + kChainC : nc;
+    }
+  }
+  __device__ __forceinline__ void advance() {
+    do {
+      if (x) {
+        x = false;
+        run();
+      } else if (++part < parts) {
+        x = true;
+        run();
+      } else {
+        t += p.group;
+        if (t >= w.t1) {
+          if (++ps == p.passes) {
+            ps = 0;
+            item += step;
+            if (item >= p.items) { live = false; return; }
+            w = Walk(item, p);
+          }
+          kt = ps * p.group + me;
+          t = w.t0;
+        }
+        open();
+      }
+    } while (i >= e);
+  }
+  __device__ __forceinline__ void next() {
+    if (++i == e) advance();
+  }
+  // the first and the last slice of a chain
+  __device__ __forceinline__ bool opens() const {
+    return x ? i == 0 || (XCHAINS && i % kChainX == 0) : i % kChainC == 0;
+  }
+  __device__ __forceinline__ bool closes() const {
+    return x ? i == nx - 1 || (XCHAINS && i % kChainX == kChainX - 1) : i + 1 == e;
+  }
+  // the chain is its result's first (x: of the tile, else of the item's pass)
+  __device__ __forceinline__ bool first_chain() const { return x ? i < kChainX : t == w.t0 && part == 0; }
+  // the last point slice of an item's pass
+  __device__ __forceinline__ bool ends() const { return !x && i == nc - 1 && t + p.group >= w.t1; }
+  __device__ __forceinline__ int plane() const { return p.planes == 1 ? 0 : i % p.planes; }
+  // first centroid (x) or point of the slice
+  __device__ __forceinline__ int row0() const {
+    const int l = (p.planes == 1 ? i : i / p.planes) * kSlice;
+    return x ? l : static_cast<int>(t * kRT) + l;
+  }
+};
+
+template <int N, bool UP>
+__device__ __forceinline__ void set_registers() {
+  if (UP) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // s0 += the low half of w, s1 += the high one (bf16, added in float32).
@@ -163,15 +273,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const WaitGuard g{p.status, abort_flag, p.limit_ns};
   const int64_t grp = blockIdx.x / p.group;
   const int me = static_cast<int>(blockIdx.x - grp * p.group);
-  const int kslices = (p.K + kSlice - 1) / kSlice;
-  // point slices of the step starting at tile t
-  auto step_slices = [&](int64_t t, int64_t t1) {
-    const int64_t r0 = t * kRT, e = (t + p.group < t1 ? t + p.group : t1) * kRT;
-    return static_cast<int>(((e < p.N ? e : p.N) - r0 + kSlice - 1) / kSlice);
-  };
+  using Slices = Cursor<WX, kRows, !OUT_BF16>;
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < kEpiWarp0) {
+    set_registers<kRegsRest, false>();
+    if (warp == 0 && lane == 0) {
       prefetch_tensormap(&ds_x);
       prefetch_tensormap(&ds_c);
       prefetch_tensormap(&cmap);
@@ -182,47 +288,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       int issued[kStages];
 #pragma unroll
       for (int i = 0; i < kStages; ++i) issued[i] = -1;
-      bool ok = true;
-      auto next = [&]() { if (++st == kStages) { st = 0; ph ^= 1u; } };
-      for (int64_t item = grp; ok && item < p.items; item += p.groups) {
-        const Walk w(item, p);
-        const int d0 = w.dt * kDT;
-        for (int ps = 0; ok && ps < p.passes; ++ps) {
-          const int kt = ps * p.group + me;
-          for (int64_t t = w.t0; ok && t < w.t1; t += p.group) {
-            if (WX && ps == 0 && t + me < w.t1) {
-              const int r0 = static_cast<int>((t + me) * kRT);
-              for (int i = 0; ok && i < kslices * p.planes; ++i) {
-                const int l = i / p.planes, pl = i - l * p.planes;
-                if (!mbar_wait(&empty[st], ph ^ 1u, g)) { ok = false; break; }
-                uint8_t* dst = ops + st * kStageB;
-                mbar_arrive_expect_tx(&full[st], kStageB);
-                tma_load_3d(dst, &cmap, d0, l * kSlice, w.b, &full[st]);
-                tma_load_3d(dst + kBoxBytes, &cmap, d0 + 64, l * kSlice, w.b, &full[st]);
-                tma_load_3d_hint(dst + kABytes, &ds_x, l * kSlice, r0, pl * p.B + w.b, &full[st], keep);
-                issued[st] = static_cast<int>(ph);
-                next();
-              }
-            }
-            if (kRows && kt < p.nkt && ok) {
-              const int n = step_slices(t, w.t1) * p.planes;
-              for (int i = 0; i < n; ++i) {
-                const int l = i / p.planes, pl = i - l * p.planes;
-                const int r0 = static_cast<int>(t * kRT + l * kSlice);
-                if (!mbar_wait(&empty[st], ph ^ 1u, g)) { ok = false; break; }
-                uint8_t* dst = ops + st * kStageB;
-                mbar_arrive_expect_tx(&full[st], kABytes + KT / 64 * kBoxBytes);
-                tma_load_3d(dst, &xmap, d0, r0, w.b, &full[st]);
-                tma_load_3d(dst + kBoxBytes, &xmap, d0 + 64, r0, w.b, &full[st]);
+      for (Slices c(p, grp, me); c.live; c.next()) {
+        if (!mbar_wait(&empty[st], ph ^ 1u, g)) break;
+        uint8_t* dst = ops + st * kStageB;
+        const int r0 = c.row0(), d0 = c.w.dt * kDT, z = c.plane() * p.B + c.w.b;
+        mbar_arrive_expect_tx(&full[st], kABytes + (c.x ? kBBytes : KT / 64 * kBoxBytes));
+        const CUtensorMap* values = c.x ? &cmap : &xmap;
+        tma_load_3d(dst, values, d0, r0, c.w.b, &full[st]);
+        tma_load_3d(dst + kBoxBytes, values, d0 + 64, r0, c.w.b, &full[st]);
+        if (c.x) {
+          tma_load_3d_hint(dst + kABytes, &ds_x, r0, static_cast<int>((c.t + me) * kRT), z, &full[st], keep);
+        } else {
 #pragma unroll
-                for (int j = 0; j < KT / 64; ++j)
-                  tma_load_3d_hint(dst + kABytes + j * kBoxBytes, &ds_c, kt * KT + j * 64, r0, pl * p.B + w.b, &full[st], drop);
-                issued[st] = static_cast<int>(ph);
-                next();
-              }
-            }
-          }
+          for (int j = 0; j < KT / 64; ++j)
+            tma_load_3d_hint(dst + kABytes + j * kBoxBytes, &ds_c, c.kt * KT + j * 64, r0, z, &full[st], drop);
         }
+        issued[st] = static_cast<int>(ph);
+        if (++st == kStages) { st = 0; ph ^= 1u; }
       }
       // copies still in flight land before the CTA can exit (at once, unless a
       // wait ran out)
@@ -232,66 +314,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < kStages; ++i)
         if (issued[i] >= 0) mbar_wait(&full[i], static_cast<uint32_t>(issued[i]), g2);
     }
-  } else if (warp == 1) {
-    if (lane == 0) {
+    if (warp == 1 && lane == 0) {
       // bf16 x bf16 -> f32; bit 15: A is MN-major, bit 16: so is B (dC)
       constexpr uint32_t idesc_x = umma_idesc(false, kDT, kRT) | (1u << 15);
       constexpr uint32_t idesc_c = umma_idesc(false, kDT, KT) | (1u << 15) | (1u << 16);
       int st = 0;
       uint32_t ph = 0, xph = 0, cph = 0;
-      bool ok = true;
-      auto next = [&]() { if (++st == kStages) { st = 0; ph ^= 1u; } };
-      for (int64_t item = grp; ok && item < p.items; item += p.groups) {
-        const Walk w(item, p);
-        for (int ps = 0; ok && ps < p.passes; ++ps) {
-          const int kt = ps * p.group + me;
-          const bool rows = kRows && kt < p.nkt;
-          uint32_t acc_c = 0;
-          if (rows) {
-            if (!mbar_wait(c_empty, cph ^ 1u, g)) { ok = false; break; }
-          }
-          for (int64_t t = w.t0; ok && t < w.t1; t += p.group) {
-            if (WX && ps == 0 && t + me < w.t1) {
-              if (!mbar_wait(x_empty, xph ^ 1u, g)) { ok = false; break; }
-              for (int i = 0; i < kslices * p.planes; ++i) {
-                if (!mbar_wait(&full[st], ph, g)) { ok = false; break; }
-                tc_fence_after();
-                const uint32_t a = smem_addr(ops + st * kStageB);
+      for (Slices c(p, grp, me); c.live; c.next()) {
+        const bool opens = c.opens();
+        if (opens && !mbar_wait(c.x ? x_empty : c_empty, (c.x ? xph : cph) ^ 1u, g)) break;
+        if (!mbar_wait(&full[st], ph, g)) break;
+        tc_fence_after();
+        const uint32_t a = smem_addr(ops + st * kStageB);
+        if (c.x) {
 #pragma unroll
-                for (int s = 0; s < kSlice / 16; ++s)
-                  umma_ss<false>(tmem, sw128_mnmajor_desc(a + s * 2048), sw128_kmajor_desc(a + kABytes + s * 32), idesc_x,
-                                 i != 0 || s != 0 ? 1u : 0u);
-                umma_commit(&empty[st]);
-                next();
-              }
-              if (!ok) break;
-              umma_commit(x_full);
-              xph ^= 1u;
-            }
-            if (rows) {
-              const int n = step_slices(t, w.t1) * p.planes;
-              for (int i = 0; i < n; ++i) {
-                if (!mbar_wait(&full[st], ph, g)) { ok = false; break; }
-                tc_fence_after();
-                const uint32_t a = smem_addr(ops + st * kStageB);
-                if (WC) {
+          for (int s = 0; s < kSlice / 16; ++s)
+            umma_ss<false>(tmem, sw128_mnmajor_desc(a + s * 2048), sw128_kmajor_desc(a + kABytes + s * 32), idesc_x,
+                           !opens || s != 0 ? 1u : 0u);
+        } else if (WC) {
 #pragma unroll
-                  for (int s = 0; s < kSlice / 16; ++s) {
-                    umma_ss<false>(tmem + kRT, sw128_mnmajor_desc(a + s * 2048),
-                                   sw128_mnmajor_desc(a + kABytes + s * 2048), idesc_c, acc_c);
-                    acc_c = 1;
-                  }
-                }
-                umma_commit(&empty[st]);
-                next();
-              }
-            }
-          }
-          if (!ok) break;
-          if (rows) {
-            umma_commit(c_full);
-            cph ^= 1u;
-          }
+          for (int s = 0; s < kSlice / 16; ++s)
+            umma_ss<false>(tmem + kRT, sw128_mnmajor_desc(a + s * 2048), sw128_mnmajor_desc(a + kABytes + s * 2048),
+                           idesc_c, !opens || s != 0 ? 1u : 0u);
+        }
+        umma_commit(&empty[st]);
+        if (++st == kStages) { st = 0; ph ^= 1u; }
+        if (c.closes()) {
+          umma_commit(c.x ? x_full : c_full);
+          if (c.x) xph ^= 1u;
+          else cph ^= 1u;
         }
       }
       umma_commit(drain);  // every MMA is done before TMEM can be released
@@ -300,133 +351,134 @@ __global__ void __launch_bounds__(kThreads, 1)
       g2.abort_flag = &never;
       mbar_wait(drain, 0u, g2);
     }
-  } else if (warp < 2 + kEpiWarps) {
-    const int q = warp & 3, half = (warp - 2) >> 2;
-    const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
+  } else if (warp < kSumWarp0) {
+    set_registers<kRegsEpi, true>();
+    const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
+    // this warp's lanes (coordinates) and columns of an accumulator
+    const uint32_t at = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * 128);
     uint32_t xph = 0, cph = 0;
+    float acc[8][16];
     bool ok = true;
-    // cols columns of an accumulator from col on, this lane's coordinate of each, to row r of out
-    auto drain_cols = [&](uint32_t col, int64_t n, int d, auto* out, uint64_t* done) {
-      n = n < 0 ? 0 : n;
+    for (Slices c(p, grp, me); ok && c.live; c.next()) {
+      if (!c.closes()) continue;
+      const int d = c.w.dt * kDT + q * 32 + lane;
+      if (!__all_sync(0xffffffffu, mbar_wait(c.x ? x_full : c_full, c.x ? xph : cph, g))) { ok = false; break; }
+      tc_fence_after();
+      if (c.x) {
+        xph ^= 1u;
+        using XT = typename std::conditional<OUT_BF16, __nv_bfloat16, float>::type;
+        const int64_t r0 = (c.t + me) * kRT + half * 128, n = p.N - r0;
+        XT* out = static_cast<XT*>(p.dX) + (static_cast<int64_t>(c.w.b) * p.N + r0) * p.D + d;
+        const bool add = !c.first_chain();
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t r[32];
-        tmem_load32(tmem + lane_off + col + static_cast<uint32_t>(c * 32), r);
-        tmem_wait32(r);
-        if (c == 3) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(done);
-        }
-        if (d < p.D) {
+        for (int j = 0; j < 8; ++j) {
+          uint32_t r[16];
+          tmem_load16(at + static_cast<uint32_t>(j * 16), r);
+          tmem_wait16(r);
+          if (j == 7) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x_empty);
+          }
+          if (d < p.D) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (c * 32 + i >= n) break;
-            const float v = __uint_as_float(r[i]) * p.alpha;
-            auto* o = out + static_cast<int64_t>(c * 32 + i) * p.D + d;
-            if constexpr (sizeof(*o) == 2) *o = __float2bfloat16_rn(v);
-            else *o = v;
+            for (int i = 0; i < 16; ++i) {
+              if (j * 16 + i >= n) break;
+              const float v = __uint_as_float(r[i]) * p.alpha;
+              XT* o = out + static_cast<int64_t>(j * 16 + i) * p.D;
+              if constexpr (OUT_BF16) *o = __float2bfloat16_rn(v);
+              else if (add) asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(o), "f"(v) : "memory");
+              else *o = v;
+            }
           }
         }
-      }
-    };
-    using XT = typename std::conditional<OUT_BF16, __nv_bfloat16, float>::type;
-    for (int64_t item = grp; ok && item < p.items; item += p.groups) {
-      const Walk w(item, p);
-      const int d = w.dt * kDT + q * 32 + lane;
-      for (int ps = 0; ok && ps < p.passes; ++ps) {
-        const int kt = ps * p.group + me;
-        if (WX && ps == 0) {
-          for (int64_t t = w.t0 + me; t < w.t1; t += p.group) {
-            if (!__all_sync(0xffffffffu, mbar_wait(x_full, xph, g))) { ok = false; break; }
-            xph ^= 1u;
-            tc_fence_after();
-            const int64_t r0 = t * kRT + half * 128;
-            drain_cols(static_cast<uint32_t>(half * 128), p.N - r0, d,
-                       static_cast<XT*>(p.dX) + (static_cast<int64_t>(w.b) * p.N + r0) * p.D, x_empty);
+      } else {
+        cph ^= 1u;
+        if (c.first_chain()) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[j][i] = 0.f;
+        }
+        if (WC && half * 128 < KT) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (j * 16 >= KT) break;
+            uint32_t r[16];
+            tmem_load16(at + static_cast<uint32_t>(kRT + j * 16), r);
+            tmem_wait16(r);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[j][i] += __uint_as_float(r[i]);
           }
         }
-        if (!ok) break;
-        if (kRows && kt < p.nkt) {
-          if (!__all_sync(0xffffffffu, mbar_wait(c_full, cph, g))) { ok = false; break; }
-          cph ^= 1u;
-          tc_fence_after();
-          const int k0 = kt * KT + half * 128;
-          const int64_t n = WC && half * 128 < KT ? (p.K - k0 < KT - half * 128 ? p.K - k0 : KT - half * 128) : 0;
-          drain_cols(static_cast<uint32_t>(kRT + half * 128), n, d,
-                     p.dC + ((static_cast<int64_t>(w.split) * p.B + w.b) * p.K + k0) * p.D, c_empty);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(c_empty);
+        if (WC && c.ends() && half * 128 < KT && d < p.D) {
+          const int k0 = c.kt * KT + half * 128;
+          float* out = p.dC + ((static_cast<int64_t>(c.w.split) * p.B + c.w.b) * p.K + k0) * p.D + d;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (j * 16 + i < KT && k0 + j * 16 + i < p.K)
+                out[static_cast<int64_t>(j * 16 + i) * p.D] = acc[j][i] * p.alpha;
         }
       }
     }
-  } else if (WB) {
+  } else {
+    set_registers<kRegsRest, false>();
+    if (WB) {
     // column sums: each warp takes its share of a slice's points for 64
     // centroids; a lane has 8 centroids (16 bytes) of every fourth of them
     constexpr int kParts = kSumWarps / (KT / 64);  // warps that share 64 centroids
     constexpr int kN = kSlice / kParts;            // points of a slice per warp
     constexpr int kFlush = 64 / kN;                // slices until a lane has summed 16 points
-    const int cw = warp - 2 - kEpiWarps, box = cw / kParts, part = cw % kParts;
+    const int cw = warp - kSumWarp0, box = cw / kParts, part = cw % kParts;
+    double sum[8] = {};
+    float s[8] = {};
+    int held = 0;
+    auto flush = [&]() {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += s[j], s[j] = 0.f;
+      held = 0;
+    };
     int st = 0;
     uint32_t ph = 0;
-    bool ok = true;
-    auto next = [&]() { if (++st == kStages) { st = 0; ph ^= 1u; } };
-    for (int64_t item = grp; ok && item < p.items; item += p.groups) {
-      const Walk w(item, p);
-      for (int ps = 0; ok && ps < p.passes; ++ps) {
-        const int kt = ps * p.group + me;
-        double sum[8] = {};
-        float s[8] = {};
-        int held = 0;
-        auto flush = [&]() {
+    for (Slices c(p, grp, me); c.live; c.next()) {
+      // dX's slices are not looked at, but waited for: a barrier's parity tells
+      // only neighbouring phases apart, so no role may skip a stage's turn
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[st], ph, g))) break;
+      if (!c.x && c.w.dt == 0) {
+        const uint8_t* bx = ops + st * kStageB + kABytes + box * kBoxBytes;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) sum[j] += s[j], s[j] = 0.f;
-          held = 0;
-        };
-        for (int64_t t = w.t0; ok && t < w.t1; t += p.group) {
-          // dX's slices are not looked at, but waited for: a barrier's parity tells
-          // only neighbouring phases apart, so no role may skip a stage's turn
-          const int nx = WX && ps == 0 && t + me < w.t1 ? kslices * p.planes : 0;
-          for (int i = 0; i < nx; ++i) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&full[st], ph, g))) { ok = false; break; }
-            if (lane == 0) mbar_arrive(&empty[st]);
-            next();
-          }
-          if (!ok) break;
-          if (kt < p.nkt) {
-            const int n = step_slices(t, w.t1) * p.planes;
-            for (int i = 0; i < n; ++i) {
-              if (!__all_sync(0xffffffffu, mbar_wait(&full[st], ph, g))) { ok = false; break; }
-              const uint8_t* bx = ops + st * kStageB + kABytes + box * kBoxBytes;
-              if (w.dt == 0) {
-#pragma unroll
-                for (int h = 0; h < kN; h += 4) {
-                  const int r = part * kN + h + (lane >> 3);
-                  const uint4 v = *reinterpret_cast<const uint4*>(bx + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-                  add_bf16x2(s[0], s[1], v.x);
-                  add_bf16x2(s[2], s[3], v.y);
-                  add_bf16x2(s[4], s[5], v.z);
-                  add_bf16x2(s[6], s[7], v.w);
-                }
-                if (++held == kFlush) flush();
-              }
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&empty[st]);
-              next();
-            }
-          }
+        for (int h = 0; h < kN; h += 4) {
+          const int r = part * kN + h + (lane >> 3);
+          const uint4 v = *reinterpret_cast<const uint4*>(bx + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+          add_bf16x2(s[0], s[1], v.x);
+          add_bf16x2(s[2], s[3], v.y);
+          add_bf16x2(s[4], s[5], v.z);
+          add_bf16x2(s[6], s[7], v.w);
         }
-        if (!ok) break;
-        if (w.dt == 0 && kt < p.nkt) {
+        if (++held == kFlush) flush();
+        if (c.ends()) {
           flush();
-          float* o = p.db + (static_cast<int64_t>(w.split * kParts + part) * p.B + w.b) * p.K;
-          const int k = kt * KT + box * 64 + lane * 8;
+          float* o = p.db + (static_cast<int64_t>(c.w.split * kParts + part) * p.B + c.w.b) * p.K;
+          const int k = c.kt * KT + box * 64 + lane * 8;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 8);
-            sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 16);
-            if (lane < 8 && k + j < p.K) o[k + j] = static_cast<float>(sum[j]);
+            double v = sum[j];
+            v += __shfl_xor_sync(0xffffffffu, v, 8);
+            v += __shfl_xor_sync(0xffffffffu, v, 16);
+            if (lane < 8 && k + j < p.K) o[k + j] = static_cast<float>(v);
+            sum[j] = 0.0;
           }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+      if (++st == kStages) { st = 0; ph ^= 1u; }
+    }
     }
   }
   __syncthreads();
@@ -596,6 +648,11 @@ cudaError_t grad_t(const GradArgs& a, const GradK& k, cudaStream_t s) {
   auto kern = k_grad<KT, OUT_BF16, WX, WC, WB>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
   if (e != cudaSuccess) return e;
+  // The warpgroups can only divide what the launch was given: a build that asks
+  // for fewer registers would wait for the rest for ever.
+  cudaFuncAttributes fa;
+  if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+  if ((fa.numRegs + 7) / 8 * 8 < kRegsLaunch) return cudaErrorInvalidKernelImage;
   count_launch();
   return launch_chained(kern, dim3(static_cast<unsigned>(k.groups * k.group)), dim3(kThreads), kSmem, s, *a.ds_x, *a.ds_c,
                         *a.cmap, *a.xmap, k);
