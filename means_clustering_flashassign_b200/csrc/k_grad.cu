@@ -208,26 +208,6 @@ __device__ __forceinline__ void add_bf16x2(float& s0, float& s1, uint32_t w) {
       : "r"(w));
 }
 
-// L2 policies: a dS line is read twice, and the second time is the last.
-__device__ __forceinline__ uint64_t policy_keep() {
-  uint64_t p;
-  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
-  return p;
-}
-__device__ __forceinline__ uint64_t policy_drop() {
-  uint64_t p;
-  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
-  return p;
-}
-__device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar,
-                                                 uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
-      "[%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar)), "l"(policy)
-      : "memory");
-}
-
 // KT centroids per dC tile (the MMA's N).
 template <int KT, bool OUT_BF16, bool WX, bool WC, bool WB>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -282,7 +262,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       prefetch_tensormap(&ds_c);
       prefetch_tensormap(&cmap);
       prefetch_tensormap(&xmap);
-      const uint64_t keep = policy_keep(), drop = policy_drop();
       int st = 0;
       uint32_t ph = 0;
       int issued[kStages];
@@ -297,11 +276,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_load_3d(dst, values, d0, r0, c.w.b, &full[st]);
         tma_load_3d(dst + kBoxBytes, values, d0 + 64, r0, c.w.b, &full[st]);
         if (c.x) {
-          tma_load_3d_hint(dst + kABytes, &ds_x, r0, static_cast<int>((c.t + me) * kRT), z, &full[st], keep);
+          tma_load_3d(dst + kABytes, &ds_x, r0, static_cast<int>((c.t + me) * kRT), z, &full[st]);
         } else {
 #pragma unroll
           for (int j = 0; j < KT / 64; ++j)
-            tma_load_3d_hint(dst + kABytes + j * kBoxBytes, &ds_c, c.kt * KT + j * 64, r0, z, &full[st], drop);
+            tma_load_3d(dst + kABytes + j * kBoxBytes, &ds_c, c.kt * KT + j * 64, r0, z, &full[st]);
         }
         issued[st] = static_cast<int>(ph);
         if (++st == kStages) { st = 0; ph ^= 1u; }
