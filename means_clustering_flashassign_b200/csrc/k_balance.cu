@@ -55,6 +55,43 @@ __device__ __forceinline__ float exp_of(float x) {
   return y;
 }
 
+// Two float32 in one 64-bit register, for the packed adds, products and
+// multiply-adds (each lane rounded as by the plain instruction): the row kernels
+// spend most of their issue slots and power on these.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// exp_of for the pair x + neg.
+__device__ __forceinline__ f32x2 exp2_of(f32x2 x, f32x2 neg) {
+  float2 v = unpack2(mul2(add2(x, neg), pack2(kLog2e, kLog2e)));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(v.x));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(v.y));
+  return pack2(v.x, v.y);
+}
+
 struct BalK {
   const int32_t* idx;
   const uint8_t* valid;
@@ -319,15 +356,31 @@ __global__ void __launch_bounds__(kThreads, resident(VEC, NC)) k_bal_rows(const 
     const float m = row_reduce<LPR, true>(max_of<BF16, VEC, NC>(raw), sm[0]);
     const float sh = m == -CUDART_INF_F ? 0.f : m;
     float s = 0.f, t = 0.f;
+    if constexpr (VEC) {
+      f32x2 s2 = pack2(0.f, 0.f), t2 = s2;
+      const f32x2 neg = pack2(-sh, -sh);
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      float x[V];
-      chunk_of<BF16, VEC, NC, V>(raw, j, x);
+      for (int j = 0; j < NC; ++j) {
+        float x[V];
+        chunk_of<BF16, VEC, NC, V>(raw, j, x);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float e = exp_of(x[i] - sh);
+        for (int i = 0; i < V; i += 2) {
+          const f32x2 e = exp2_of(pack2(x[i], x[i + 1]), neg);
+          s2 = add2(s2, e);
+          t2 = fma2(e, pack2(f[j * V + i], f[j * V + i + 1]), t2);
+        }
+      }
+      const float2 ss = unpack2(s2), tt = unpack2(t2);
+      s = ss.x + ss.y;
+      t = tt.x + tt.y;
+    } else {
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        float x[V];
+        chunk_of<BF16, VEC, NC, V>(raw, j, x);
+        const float e = exp_of(x[0] - sh);
         s += e;
-        t = fmaf(e, f[j * V + i], t);
+        t = fmaf(e, f[j], t);
       }
     }
     s = row_reduce<LPR, false>(s, sm[1]);
@@ -380,8 +433,17 @@ __global__ void __launch_bounds__(kThreads, resident(VEC, NC)) k_bal_grad(const 
       if (c >= p.K) continue;
       float x[V];
       chunk_of<BF16, VEC, NC, V>(raw, j, x);
+      if constexpr (VEC) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) x[k] = now ? exp_of(x[k] - l0) * (f[j * V + k] - rc) : 0.f;
+        for (int k = 0; k < V; k += 2) {
+          const float2 v = unpack2(mul2(exp2_of(pack2(x[k], x[k + 1]), pack2(-l0, -l0)),
+                                        add2(pack2(f[j * V + k], f[j * V + k + 1]), pack2(-rc, -rc))));
+          x[k] = now ? v.x : 0.f;
+          x[k + 1] = now ? v.y : 0.f;
+        }
+      } else {
+        x[0] = now ? exp_of(x[0] - l0) * (f[j] - rc) : 0.f;
+      }
       if constexpr (VEC && BF16) {
         uint32_t w[4];
 #pragma unroll
