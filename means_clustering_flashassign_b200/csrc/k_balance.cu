@@ -104,6 +104,7 @@ struct BalK {
   float* dot;
   double* part;        // [B][nblk]
   unsigned int* done;  // [B] blocks that have added their part
+  unsigned int* status;
   const float* grad;
 };
 
@@ -116,6 +117,7 @@ __global__ void __launch_bounds__(kThreads) k_bal_zero(BalK p, int64_t nc, int B
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   for (int64_t j = i; j < nc; j += static_cast<int64_t>(gridDim.x) * kThreads) p.counts[j] = 0;
   if (i < B) p.rows[i] = 0, p.done[i] = 0;
+  if (i == 0) *p.status = 0;
 }
 
 // counts[b][k] += picks of valid points; rows[b] += valid points.  Blocks of an
@@ -153,6 +155,7 @@ __global__ void __launch_bounds__(SOLO ? kSolo : kThreads) k_bal_count(BalK p, i
   if (SOLO) {
     for (int k = threadIdx.x; k < p.K; k += kN) counts[k] = hist[k];
     if (threadIdx.x == 0) p.rows[b] = valid_rows, p.done[b] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
   } else {
     if (local)
       for (int k = threadIdx.x; k < p.K; k += kN)
@@ -641,6 +644,7 @@ BalK make_k(const BalanceArgs& a) {
   k.dot = a.dot;
   k.part = a.part;
   k.done = a.done;
+  k.status = a.status;
   k.grad = a.grad;
   return k;
 }

@@ -33,6 +33,12 @@ int sfail(int code, const char* fmt, ...) {
 constexpr size_t kAlign = 256;
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// On boundaries of its elements (null counts as aligned).
+bool aligned_to(const void* p, int dtype) {
+  return reinterpret_cast<uintptr_t>(p) % (dtype == KM_BF16 ? 2 : 4) == 0;
+}
+template <typename... P>
+bool aligned_words(const P*... p) { return (aligned_to(p, KM_F32) && ...); }
 int64_t ceil8(int64_t v) { return (v + 7) / 8 * 8; }
 
 constexpr int kMaxD = 1 << 16;
@@ -172,6 +178,7 @@ int km_quantize(const void* X, int B, int64_t N, int D, int dtype, uint8_t* q, u
     return sfail(KM_ERR_INVALID_ARG, "X, q and scale are required");
   }
   if (!aligned16(q)) return sfail(KM_ERR_INVALID_ARG, "q must be 16-byte aligned");
+  if (!aligned_to(X, dtype)) return sfail(KM_ERR_INVALID_ARG, "X must be aligned to its elements");
   if ((r = check_device_once()) != KM_OK) return r;
   SOFT_CUDA(launch_quantize(X, dtype, static_cast<int64_t>(B) * N, D, q, scale, static_cast<cudaStream_t>(stream)));
   return KM_OK;
@@ -187,6 +194,7 @@ int km_dequantize(const uint8_t* q, const uint8_t* scale, int B, int64_t N, int 
     return sfail(KM_ERR_INVALID_ARG, "q, scale and X are required");
   }
   if (!aligned16(q)) return sfail(KM_ERR_INVALID_ARG, "q must be 16-byte aligned");
+  if (!aligned_to(X, dtype)) return sfail(KM_ERR_INVALID_ARG, "X must be aligned to its elements");
   if ((r = check_device_once()) != KM_OK) return r;
   SOFT_CUDA(launch_dequantize(q, scale, dtype, static_cast<int64_t>(B) * N, D, X, static_cast<cudaStream_t>(stream)));
   return KM_OK;
@@ -199,6 +207,8 @@ int km_scores(const uint8_t* xq, const uint8_t* xs, const uint8_t* cq, const uin
   if (N != 0 && (!xq || !xs || !S)) return sfail(KM_ERR_INVALID_ARG, "xq, xs and S are required");
   if (!cq || !cs) return sfail(KM_ERR_INVALID_ARG, "cq and cs are required");
   if (!aligned16(xq) || !aligned16(cq)) return sfail(KM_ERR_INVALID_ARG, "xq and cq must be 16-byte aligned");
+  if (!aligned_to(S, dtype) || !aligned_words(bias))
+    return sfail(KM_ERR_INVALID_ARG, "S and bias must be aligned to their elements");
   SoftCtx c;
   int r = soft_prepare(c, KM_SOFT_SCORES, B, N, D, K, dtype, workspace, workspace_bytes, stream);
   if (r != KM_OK) return r;
@@ -228,6 +238,8 @@ int km_scores_grad(const void* dS, const uint8_t* xq, const uint8_t* xs, const u
   if (dx_dtype != KM_F32 && dx_dtype != KM_BF16) return sfail(KM_ERR_INVALID_ARG, "unknown dtype %d of dX", dx_dtype);
   if (!aligned16(dS) || !aligned16(xq) || !aligned16(cq))
     return sfail(KM_ERR_INVALID_ARG, "dS, xq and cq must be 16-byte aligned");
+  if (!aligned_to(dX, dx_dtype) || !aligned_words(dC, dbias))
+    return sfail(KM_ERR_INVALID_ARG, "dX, dC and dbias must be aligned to their elements");
   SoftCtx c;
   int r = soft_prepare(c, KM_SOFT_SCORES_GRAD, B, N, D, K, dtype, workspace, workspace_bytes, stream);
   if (r != KM_OK) return r;
@@ -286,6 +298,8 @@ int km_balance(const void* S, const int32_t* idx, const uint8_t* valid, int B, i
   if (!loss || !counts || !rows) return sfail(KM_ERR_INVALID_ARG, "loss, counts and rows are required");
   if (T < 1 || T > kMaxT) return sfail(KM_ERR_INVALID_ARG, "need 1 <= T <= %d (T=%d)", kMaxT, T);
   if (!aligned16(S)) return sfail(KM_ERR_INVALID_ARG, "S must be 16-byte aligned");
+  if (!aligned_words(idx, loss, counts, rows, lse, dot))
+    return sfail(KM_ERR_INVALID_ARG, "idx, loss, counts, rows, lse and dot must be 4-byte aligned");
   if (N * static_cast<int64_t>(T) >= (int64_t(1) << 31))
     return sfail(KM_ERR_UNSUPPORTED, "N * T must be below 2^31 (a count could pass int32)");
   SoftCtx c;
@@ -307,6 +321,7 @@ int km_balance(const void* S, const int32_t* idx, const uint8_t* valid, int B, i
   a.dot = dot;
   a.part = reinterpret_cast<double*>(c.ws + c.l.off_bal);
   a.done = reinterpret_cast<unsigned int*>(c.ws + c.l.off_done);
+  a.status = c.status();
   SOFT_CUDA(launch_balance(a, c.s));
   return KM_OK;
 }
@@ -320,6 +335,8 @@ int km_balance_grad(const void* S, const uint8_t* valid, const int32_t* counts, 
   if (!counts || !rows) return sfail(KM_ERR_INVALID_ARG, "counts and rows are required");
   if (T < 1 || T > kMaxT) return sfail(KM_ERR_INVALID_ARG, "need 1 <= T <= %d (T=%d)", kMaxT, T);
   if (!aligned16(S) || !aligned16(dS)) return sfail(KM_ERR_INVALID_ARG, "S and dS must be 16-byte aligned");
+  if (!aligned_words(counts, rows, lse, dot, grad))
+    return sfail(KM_ERR_INVALID_ARG, "counts, rows, lse, dot and grad must be 4-byte aligned");
   int r = check_shape(B, N, 1, K, dtype);
   if (r != KM_OK) return r;
   if ((r = check_device_once()) != KM_OK) return r;

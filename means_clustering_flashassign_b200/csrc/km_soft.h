@@ -129,6 +129,7 @@ struct BalanceArgs {
   float* dot;
   double* part;        // [B][balance_blocks]
   unsigned int* done;  // [B]
+  unsigned int* status;  // cleared
   // gradient only
   const float* grad;  // [B] or null (1)
   void* dS;

@@ -462,7 +462,8 @@ def test_the_run_of_them_together():
     # S and dS are rounded to bf16 (2^-8 each): S of size up to a few makes exp err by |S| 2^-8
     smax = float(S.detach().abs().max())
     rel = 2 * (smax + 1) * 2.0 ** -8
-    assert abs(float(loss) - float(ref)) <= rel * float(ref)
+    ref = float(ref.detach())
+    assert abs(float(loss) - ref) <= rel * ref
     for got, want in ((dX, xd.grad), (dC, cd.grad), (db, bias.grad)):
         err = (got.double() - want).norm() / want.norm()
         assert err <= 2 * rel
@@ -522,6 +523,60 @@ def test_workspaces_report_no_timeout():
     assert km.workspace_status(ws) == 0
     km.scores_grad(randn(g, 1000, 300, dtype=torch.bfloat16), qx, qc, workspace=ws)
     assert km.workspace_status(ws) == 0
+    for n in (1000, 50000):   # both ways of counting
+        ws.fill_(255)
+        km.balance(randn(g, n, 30), torch.zeros(n, dtype=torch.int32, device=DEV), workspace=ws)
+        assert km.workspace_status(ws) == 0
+
+
+def test_bytes_behind_the_rows_do_not_matter():
+    g = gen(26)
+    for D in (40, 129, 200):
+        X, C = randn(g, 300, D), randn(g, 70, D)
+        qx, qc = km.quantize(X), km.quantize(C)
+        ld = (D + 15) // 16 * 16
+        dS = randn(g, 300, 70, dtype=torch.bfloat16)
+        ref = (km.scores(qx, qc), *km.scores_grad(dS, qx, qc), km.dequantize(qx))
+
+        def dirty(q):
+            data = torch.full((q.data.shape[0], ld), 0x7f, dtype=torch.uint8, device=DEV)   # NaN bytes
+            data[:, :D] = q.data.view(torch.uint8)
+            return km.Quantized(data.view(torch.float8_e4m3fn)[:, :D], q.scale)
+        got = (km.scores(dirty(qx), dirty(qc)), *km.scores_grad(dS, dirty(qx), dirty(qc)), km.dequantize(dirty(qx)))
+        assert all(torch.equal(a, b) for a, b in zip(ref, got))
+
+
+def test_gradients_of_blocks_that_are_not_finite():
+    """A point's NaN block reaches dC's columns of that block, a centroid's NaN
+    block dX's; nothing else."""
+    g = gen(27)
+    X, C = randn(g, 300, 300), randn(g, 90, 300)
+    X[7, 130] = float("inf")
+    C[5, 299] = float("nan")
+    dX, dC, db = km.scores_grad(randn(g, 300, 90), km.quantize(X), km.quantize(C))
+    assert torch.isnan(dC[:, 128:256]).all() and torch.isfinite(dC[:, :128]).all() and torch.isfinite(dC[:, 256:]).all()
+    assert torch.isnan(dX[:, 256:]).all() and torch.isfinite(dX[:, :256]).all()
+    assert torch.isfinite(db).all()
+
+
+@pytest.mark.parametrize("N,D,K,dtype", [(40000, 64, 300, torch.bfloat16), (9000, 32, 5000, torch.float32),
+                                         (2000, 24, 40000, torch.float32), (300000, 16, 8, torch.float32)])
+def test_long_sums_keep_their_precision(N, D, K, dtype):
+    """Sums over many points and many centroids: chains of at most 32 (dC) or 64
+    (float32 dX) MMAs, each losing at most 2^-23 of its magnitudes, joined by
+    rounded adds of which there are at most sqrt(terms / 512) + 40 in effect
+    (rounding errors of either sign); the error of the whole result, in norms,
+    against the size of its terms."""
+    g = gen(N)
+    X, C = randn(g, N, D) + 1.0, randn(g, K, D) - 1.0
+    qx, qc = km.quantize(X), km.quantize(C)
+    dS = (torch.rand(N, K, generator=g, device=DEV) * 1e-4).to(dtype)   # all of one sign: no cancellation to hide behind
+    dX, dC, _ = km.scores_grad(dS, qx, qc, dtype=torch.float32)
+    x, c, d = values(qx), values(qc), dS.double()
+    for got, ref, terms in ((dX, d @ c, K), (dC, d.mT @ x, N)):
+        chain = min(64, terms // 16 * (3 if dtype == torch.float32 else 1) + 1)
+        tol = (chain * 2.0 ** -23 + ((terms / 512) ** 0.5 + 40) * 2.0 ** -24)
+        assert (got.double() - ref).norm() <= tol * ref.norm()
 
 
 @pytest.mark.parametrize("call,spec", [("quantize", "launch"), ("scores", "launch"), ("grad", "launch"),

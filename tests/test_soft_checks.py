@@ -144,6 +144,11 @@ def test_c_entries_refuse_bad_calls_before_the_device():
     bgrad = lambda s=p, ds=p, r=p, t=1: L.km_balance_grad(s, None, p, r, p, p, None, 1, 4, 4, t, km.F32, ds, None)  # noqa: E731
     assert bgrad(s=None) == INVALID and bgrad(ds=None) == INVALID and bgrad(r=None) == INVALID
     assert bgrad(ds=odd) == INVALID and bgrad(t=0) == INVALID
+    one = ctypes.c_void_p(a + 1)   # between elements
+    assert L.km_quantize(one, 1, 4, 8, km.BF16, p, p, None) == INVALID
+    assert L.km_dequantize(p, p, 1, 4, 8, km.F32, ctypes.c_void_p(a + 2), None) == INVALID
+    assert scores(s=one) == INVALID and grad(dx=one) == INVALID and grad(dc=one) == INVALID
+    assert bal(i=one) == INVALID and bal(loss=one) == INVALID and bgrad(r=one) == INVALID
 
 
 def test_valid_calls_without_a_gpu_report_the_device():
