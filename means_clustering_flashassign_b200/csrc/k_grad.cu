@@ -23,6 +23,11 @@
 // Both accumulators (256 columns each) stay in tensor memory side by side, so
 // that dX's epilogue runs under dC's MMAs.
 //
+// The bf16 operands come from a pass over the 8-bit ones (k_grad_prep, 76 us for
+// 1M x 128 points).  Converting slices in shared memory instead, by two warps or by
+// eight, made this kernel slower by more than the pass takes (a slice then waits
+// for its conversion, about 3000 cycles from landing to operand).
+//
 // Structure: warp 0 TMA, warp 1 MMA, warps 4..11 epilogue, warps 12..15 column
 // sums (dbias, from the staged dS slices of the dC product: float32 over 16
 // points, those joined in float64).  The epilogue warps hold a whole dC tile in
@@ -521,7 +526,7 @@ __device__ __forceinline__ void prep_values(const uint8_t* q, const uint8_t* sca
   for (int64_t base = static_cast<int64_t>(blk) * (kT * kU) + threadIdx.x; base < pieces;
        base += static_cast<int64_t>(nblk) * (kT * kU)) {
     uint2 u[kU];
-    float s[kU];
+    uint32_t s[kU];
     int64_t to[kU];
 #pragma unroll
     for (int k = 0; k < kU; ++k) {
@@ -531,7 +536,7 @@ __device__ __forceinline__ void prep_values(const uint8_t* q, const uint8_t* sca
       const int64_t row = small ? static_cast<int64_t>(static_cast<uint32_t>(at) / static_cast<uint32_t>(gpr)) : at / gpr;
       const int c = static_cast<int>(at - row * gpr) * 8;
       u[k] = __ldcs(reinterpret_cast<const uint2*>(q + row * ld + c));
-      s[k] = e8m0(__ldg(scale + row * nb + c / kQBlock));
+      s[k] = __ldg(scale + row * nb + c / kQBlock);
       to[k] = row * ldd + c;
     }
 #pragma unroll

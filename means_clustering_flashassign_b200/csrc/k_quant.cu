@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kQThreads) k_dequantize(const uint8_t* __restr
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * (kQThreads * kDU) + threadIdx.x;
        base < static_cast<int64_t>(groups); base += step) {
     uint32_t u[kDU][kDE / 4];
-    float s[kDU];
+    uint32_t s[kDU];
     int64_t row[kDU];
     int c0[kDU];
 #pragma unroll
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kQThreads) k_dequantize(const uint8_t* __restr
       } else {
         u[k][0] = __ldcs(reinterpret_cast<const uint32_t*>(src));
       }
-      s[k] = e8m0(__ldg(scale + static_cast<int64_t>(r) * nb + c0[k] / kQBlock));
+      s[k] = __ldg(scale + static_cast<int64_t>(r) * nb + c0[k] / kQBlock);
     }
 #pragma unroll
     for (int k = 0; k < kDU; ++k) {
@@ -186,13 +186,13 @@ __global__ void __launch_bounds__(kQThreads) k_dequantize(const uint8_t* __restr
       if constexpr (VEC && BF16) {  // whole pieces: D is a multiple of 8
         *reinterpret_cast<uint4*>(out) = e4m3x8_bf16(make_uint2(u[k][0], u[k][1]), s[k]);
       } else if constexpr (VEC) {
-        const float2 a = e4m3x2(u[k][0], s[k]), b = e4m3x2(u[k][0] >> 16, s[k]);
+        const float2 a = e4m3x2(u[k][0], e8m0(s[k])), b = e4m3x2(u[k][0] >> 16, e8m0(s[k]));
         *reinterpret_cast<float4*>(out) = make_float4(a.x, a.y, b.x, b.y);
       } else {
         float v[kDE];
 #pragma unroll
         for (int i = 0; i < kDE / 2; ++i) {
-          const float2 f = e4m3x2(u[k][i / 2] >> (16 * (i & 1)), s[k]);
+          const float2 f = e4m3x2(u[k][i / 2] >> (16 * (i & 1)), e8m0(s[k]));
           v[2 * i] = f.x;
           v[2 * i + 1] = f.y;
         }

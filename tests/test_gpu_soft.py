@@ -598,3 +598,37 @@ def test_injected_launch_failures(call, spec, monkeypatch):
     monkeypatch.delenv("KM_FAULT")
     fns[call]()
     torch.cuda.synchronize()
+
+
+def test_every_8_bit_value_under_every_kind_of_scale():
+    """All 256 bytes (NaN among them) under the scales 2^-127, 2^-117, 1, 2^7, 2^8,
+    2^120, 2^127 and NaN: what dequantize gives, and what the gradients multiply
+    by (dS = 1 at one centroid or point each)."""
+    scales = torch.tensor([0, 10, 127, 134, 135, 247, 254, 255], dtype=torch.uint8, device=DEV)
+    data = torch.arange(256, dtype=torch.uint8, device=DEV).view(2, 128).repeat(8, 1).view(torch.float8_e4m3fn)
+    q = km.Quantized(data, scales.repeat_interleave(2)[:, None].contiguous().view(torch.float8_e8m0fnu))
+    v = values(q)
+
+    def same(got, dtype):
+        # one rounding to the type, which some scales need (an overflow rounds to infinity)
+        want = v.to(torch.float32).to(dtype)
+        return torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(got.nan_to_num(7.0), want.nan_to_num(7.0))
+    big = scales.repeat_interleave(2) == 0   # products below 2^-126 may leave bf16's or the MMA's range
+    assert same(km.dequantize(q, torch.float32), torch.float32)
+    got = km.dequantize(q, torch.bfloat16)
+    keep = ~big
+    assert torch.equal(got[keep].nan_to_num(7.0), v.float().bfloat16()[keep].nan_to_num(7.0))
+    eye = torch.eye(16, dtype=torch.bfloat16, device=DEV)
+    finite = (scales.repeat_interleave(2) > 0) & (scales.repeat_interleave(2) < 247)
+    f = km.Quantized(q.data[finite].contiguous(), q.scale[finite].contiguous())
+    n = int(finite.sum())
+    w = values(f)
+    nan = torch.isnan(w)
+    one = km.quantize(torch.ones(n, 128, device=DEV))
+    dX, _, _ = km.scores_grad(eye[:n, :n].contiguous(), one, f, dtype=torch.float32)
+    _, dC, _ = km.scores_grad(eye[:n, :n].contiguous(), f, one, dtype=torch.float32)
+    # a NaN in a column of the operand reaches every row of it through 0 * NaN
+    col = nan.any(0)
+    for got in (dX, dC):
+        assert torch.isnan(got[:, col]).all()
+        assert torch.equal(got[:, ~col].double(), w[:, ~col])
