@@ -23,8 +23,9 @@
 //   warps 4..7    scales: the scale bytes from global memory into TMEM, four
 //                 blocks at a time, in the layout the MMA reads (row r in lane
 //                 r % 32, column r / 32, repeated in each lane quarter);
-//   warps 8..19   epilogue: three groups, one per accumulator; alpha, bias,
-//                 rounding, and whole 128-byte lines to S through shared memory.
+//   warps 8..     epilogue: three groups of four, one per accumulator (one group for
+//                 all of them where points are wide); alpha, bias, rounding, and whole
+//                 128-byte lines to S through shared memory.
 // Every wait is bounded in time (km_ptx.cuh).
 #include "km_internal.h"
 #include "km_soft.h"
@@ -47,7 +48,7 @@ constexpr int kBarBytes = 320;
 // (three 16 KB blocks per 128 coordinates instead of four: L2's bandwidth to
 // the SMs bounds it); stages of one block of each, stages of scales
 constexpr int kWideRun = 2;
-constexpr int kStages = 3;
+constexpr int kStages = 4;
 constexpr int kStageOps = (1 + kWideRun) * kOpBytes;
 constexpr int kSfStages = 8;
 constexpr int kSfCols = 4 * (1 + kWideRun);  // 4 TMEM columns of scales per tile
@@ -56,8 +57,12 @@ constexpr int kSfCols = 4 * (1 + kWideRun);  // 4 TMEM columns of scales per til
 constexpr int kNearTiles = 10;
 constexpr int kNearSfA = 4;
 constexpr int kNearMaxRun = 8;           // centroid tiles held (and 4 TMEM columns of scales for each)
-constexpr size_t kSmem = 1024 + kNearTiles * kOpBytes + kEpiWarps * kEpiBytes + kBarBytes;
-static_assert(kNearTiles * kOpBytes >= kStages * kStageOps && kWideRun <= kAccs, "one shared-memory layout for both kernels");
+constexpr int kNearOps = kNearTiles * kOpBytes, kWideOps = kStages * kStageOps;
+constexpr int kWideEpiWarps = 4;         // one group for all accumulators: a unit of wide points is long
+constexpr size_t smem_of(int ops, int epi_warps) { return 1024 + ops + epi_warps * kEpiBytes + kBarBytes; }
+constexpr size_t kNearSmem = smem_of(kNearOps, kEpiWarps), kWideSmem = smem_of(kWideOps, kWideEpiWarps);
+constexpr int kWideThreads = 32 * (8 + kWideEpiWarps);
+static_assert(kNearSmem <= 232448 && kWideSmem <= 232448 && kWideRun <= kAccs, "shared memory");
 static_assert(kSfBase + kSfStages * kSfCols <= kTmemCols && kSfBase + 4 * (kNearMaxRun + kNearSfA) <= kTmemCols, "TMEM");
 
 struct ScoresK {
@@ -72,6 +77,7 @@ struct ScoresK {
   int64_t runs;    // runs of centroid tiles per instance
   int64_t units;   // k_scores_wide: (instance, point tile, run) triples
   void* S;
+  bool xwords, cwords;  // k_scores_wide: scale_word
   bool boxes;  // S goes out as boxes of its tensor map (rows of 16 bytes)
   bool pairs;  // else, bf16: two at a time (rows of 4 bytes)
   unsigned int* status;
@@ -116,17 +122,29 @@ __device__ __forceinline__ void tmem_store4(uint32_t taddr, const uint32_t (&r)[
                : "memory");
 }
 
-// The scales of blocks k0 .. k0 + 3 of a row (1 where there is no such row or block).
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int64_t row, int64_t rows, int nb, int k0) {
+// The scales of blocks k0 .. k0 + 3 of a row (1 where there is no such row or
+// block); words: rows of scales are of 4 bytes.
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int64_t row, int64_t rows, int nb, int k0, bool words) {
   uint32_t w = 0x7f7f7f7fu;
   if (row < rows) {
     const uint8_t* p = s + row * nb + k0;
+    if (words) return __ldg(reinterpret_cast<const uint32_t*>(p));
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (k0 + i < nb) w = (w & ~(0xffu << (8 * i))) | (static_cast<uint32_t>(__ldg(p + i)) << (8 * i));
   }
   return w;
 }
+// A tile's scales of four blocks as its four TMEM columns hold them (this lane's
+// rows: 32 j + lane).
+struct TileScales {
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const uint8_t* s, int64_t row0, int64_t rows, int nb, int k0, bool words, int lane) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = scale_word(s, row0 + 32 * j + lane, rows, nb, k0, words);
+  }
+  __device__ __forceinline__ void store(uint32_t taddr) const { tmem_store4(taddr, w); }
+};
 
 // The bias of the tile's columns for this warp, 4 per lane (0 where there is none).
 __device__ __forceinline__ float4 load_bias(const ScoresK& p, int b, int n0, int lane) {
@@ -209,7 +227,7 @@ struct Bars {
   uint32_t tmem;
   int abort_flag;
 };
-static_assert(sizeof(Bars) <= kBarBytes && kSmem <= 232448, "shared memory");
+static_assert(sizeof(Bars) <= kBarBytes, "barrier space");
 
 struct Setup {
   uint8_t* ops;
@@ -217,11 +235,11 @@ struct Setup {
   Bars* bars;
   uint32_t tmem;
 };
-__device__ __forceinline__ Setup scores_setup(uint8_t* smem_raw) {
+__device__ __forceinline__ Setup scores_setup(uint8_t* smem_raw, int ops_bytes, int epi_warps) {
   Setup s;
   s.ops = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  s.epi = s.ops + kNearTiles * kOpBytes;
-  s.bars = reinterpret_cast<Bars*>(s.epi + kEpiWarps * kEpiBytes);
+  s.epi = s.ops + ops_bytes;
+  s.bars = reinterpret_cast<Bars*>(s.epi + epi_warps * kEpiBytes);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&s.bars->full[i], 1);
@@ -266,13 +284,6 @@ __device__ __forceinline__ void settle(uint64_t* bar, uint32_t phase, const Wait
   WaitGuard g2 = g;
   g2.abort_flag = &never;
   mbar_wait(bar, phase, g2);
-}
-__device__ __forceinline__ void store_scales(uint32_t taddr, const uint8_t* s, int64_t row0, int64_t rows, int nb, int k0,
-                                             int lane) {
-  uint32_t w[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) w[j] = scale_word(s, row0 + 32 * j + lane, rows, nb, k0);
-  tmem_store4(taddr, w);
 }
 __device__ __forceinline__ void publish_scales(uint64_t* bar, int lane) {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -330,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_scores_near(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap cmap,
              const __grid_constant__ CUtensorMap smap, const ScoresK p) {
   extern __shared__ uint8_t smem_raw[];
-  const Setup su = scores_setup(smem_raw);
+  const Setup su = scores_setup(smem_raw, kNearOps, kEpiWarps);
   Bars& bars = *su.bars;
   const WaitGuard g{p.status, &bars.abort_flag, p.limit_ns};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -416,20 +427,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t sph = 0, bph = 0;
     bool fresh = true;
     for (UnitPos q = first; q != end; q.next(p)) {
+      TileScales x;
+      x.load(p.xs + static_cast<int64_t>(q.b) * p.N * nb, q.m * kBM, p.N, nb, 0, false, lane);
       if (fresh || q.m == 0) {
         fresh = false;
         if (!__all_sync(0xffffffffu, mbar_wait(&bars.b_empty, bph ^ 1u, g))) break;
         bph ^= 1u;
         tc_fence_after();
-        for (int j = 0; j < q.j1 - q.j0; ++j)
-          store_scales(sfb + lane_off + static_cast<uint32_t>(4 * j), p.cs + static_cast<int64_t>(q.b) * p.K * nb,
-                       static_cast<int64_t>(q.j0 + j) * kBN, p.K, nb, 0, lane);
+        for (int j = 0; j < q.j1 - q.j0; ++j) {
+          TileScales c;
+          c.load(p.cs + static_cast<int64_t>(q.b) * p.K * nb, static_cast<int64_t>(q.j0 + j) * kBN, p.K, nb, 0, false, lane);
+          c.store(sfb + lane_off + static_cast<uint32_t>(4 * j));
+        }
         publish_scales(&bars.sfb_full, lane);
       }
       if (!__all_sync(0xffffffffu, mbar_wait(&bars.sf_empty[ss], sph ^ 1u, g))) break;
       tc_fence_after();
-      store_scales(sfa + lane_off + static_cast<uint32_t>(4 * ss), p.xs + static_cast<int64_t>(q.b) * p.N * nb, q.m * kBM,
-                   p.N, nb, 0, lane);
+      x.store(sfa + lane_off + static_cast<uint32_t>(4 * ss));
       publish_scales(&bars.sf_full[ss], lane);
       if (++ss == kNearSfA) { ss = 0; sph ^= 1u; }
     }
@@ -460,11 +474,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kWideThreads, 1)
     k_scores_wide(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap cmap,
              const __grid_constant__ CUtensorMap smap, const ScoresK p) {
   extern __shared__ uint8_t smem_raw[];
-  const Setup su = scores_setup(smem_raw);
+  const Setup su = scores_setup(smem_raw, kWideOps, kWideEpiWarps);
   Bars& bars = *su.bars;
   const WaitGuard g{p.status, &bars.abort_flag, p.limit_ns};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -542,41 +556,54 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     int ss = 0;
     uint32_t sph = 0;
-    bool ok = true;
-    for (int64_t t = blockIdx.x; ok && t < p.units; t += gridDim.x) {
+    // four blocks of every tile at a time, fetched one such step ahead (their
+    // latency, one tile after the other, was most of a unit's time)
+    TileScales now[1 + kWideRun], next[1 + kWideRun];
+    auto fetch = [&](int64_t t, int k0) {
+      if (t >= p.units) return;
       const TilePos tp = tile_pos(t, p);
-      for (int k0 = 0; k0 < nb; k0 += 4) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars.sf_empty[ss], sph ^ 1u, g))) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t a = su.tmem + lane_off + kSfBase + static_cast<uint32_t>(ss * kSfCols);
-        store_scales(a, p.xs + static_cast<int64_t>(tp.b) * p.N * nb, tp.m0, p.N, nb, k0, lane);
-        for (int j = 0; j < tp.n; ++j)
-          store_scales(a + static_cast<uint32_t>(4 * (1 + j)), p.cs + static_cast<int64_t>(tp.b) * p.K * nb,
-                       tp.n0 + j * kBN, p.K, nb, k0, lane);
-        publish_scales(&bars.sf_full[ss], lane);
-        if (++ss == kSfStages) { ss = 0; sph ^= 1u; }
+      next[0].load(p.xs + static_cast<int64_t>(tp.b) * p.N * nb, tp.m0, p.N, nb, k0, p.xwords, lane);
+#pragma unroll
+      for (int j = 0; j < kWideRun; ++j)
+        next[1 + j].load(p.cs + static_cast<int64_t>(tp.b) * p.K * nb, tp.n0 + j * kBN, p.K, nb, k0, p.cwords, lane);
+    };
+    int64_t t = blockIdx.x;
+    int k0 = 0;
+    fetch(t, k0);
+    while (t < p.units) {
+#pragma unroll
+      for (int j = 0; j <= kWideRun; ++j) now[j] = next[j];
+      if ((k0 += 4) >= nb) {
+        k0 = 0;
+        t += gridDim.x;
       }
+      fetch(t, k0);
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars.sf_empty[ss], sph ^ 1u, g))) break;
+      tc_fence_after();
+      const uint32_t a = su.tmem + lane_off + kSfBase + static_cast<uint32_t>(ss * kSfCols);
+#pragma unroll
+      for (int j = 0; j <= kWideRun; ++j) now[j].store(a + static_cast<uint32_t>(4 * j));  // (one of them unused at a ragged end)
+      publish_scales(&bars.sf_full[ss], lane);
+      if (++ss == kSfStages) { ss = 0; sph ^= 1u; }
     }
   } else if (warp >= 8) {
-    const int q4 = warp & 3, grp = (warp - 8) >> 2;
-    const uint32_t tm = su.tmem + (static_cast<uint32_t>(q4 * 32) << 16) + static_cast<uint32_t>(grp * kBN);
+    const int q4 = warp & 3;
+    const uint32_t tm = su.tmem + (static_cast<uint32_t>(q4 * 32) << 16);
     uint8_t* stage = su.epi + (warp - 8) * kStageBytes;
-    float* bias = reinterpret_cast<float*>(su.epi + kEpiWarps * kStageBytes) + (warp - 8) * kBN;
+    float* bias = reinterpret_cast<float*>(su.epi + kWideEpiWarps * kStageBytes) + (warp - 8) * kBN;
     uint32_t aph = 0;
     int ab = 0;
     bool ok = true;
     for (int64_t t = blockIdx.x; ok && t < p.units; t += gridDim.x) {
       const TilePos tp = tile_pos(t, p);
       for (int j = 0; j < tp.n; ++j) {
-        const bool mine = ab == grp;
-        if (++ab == kAccs) ab = 0;
-        if (!mine) continue;
         const int n0 = tp.n0 + j * kBN;
         const float4 bias4 = load_bias(p, tp.b, n0, lane);
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars.a_full[grp], aph, g))) { ok = false; break; }
-        aph ^= 1u;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars.a_full[ab], aph, g))) { ok = false; break; }
         tc_fence_after();
-        emit_tile<BF16>(p, &smap, tp.b, tp.m0 + q4 * 32, n0, tm, &bars.a_empty[grp], stage, bias, bias4, lane);
+        emit_tile<BF16>(p, &smap, tp.b, tp.m0 + q4 * 32, n0, tm + static_cast<uint32_t>(ab * kBN), &bars.a_empty[ab], stage,
+                        bias, bias4, lane);
+        if (++ab == kAccs) { ab = 0; aph ^= 1u; }
       }
     }
     stage_reusable(lane);
@@ -603,6 +630,8 @@ cudaError_t launch_scores(const ScoresArgs& a, cudaStream_t s) {
   k.nt = (a.K + kBN - 1) / kBN;
   k.ntiles = k.mt * k.nt * a.B;
   k.S = a.S;
+  k.xwords = k.nb % 4 == 0 && reinterpret_cast<uintptr_t>(a.xs) % 4 == 0;
+  k.cwords = k.nb % 4 == 0 && reinterpret_cast<uintptr_t>(a.cs) % 4 == 0;
   k.boxes = a.smap != nullptr;
   k.pairs = a.K % 2 == 0 && reinterpret_cast<uintptr_t>(a.S) % 4 == 0;
   k.status = a.status;
@@ -626,11 +655,13 @@ cudaError_t launch_scores(const ScoresArgs& a, cudaStream_t s) {
   }
   const bool bf16 = a.dtype == kDtypeBF16;
   auto kern = near ? (bf16 ? k_scores_near<true> : k_scores_near<false>) : (bf16 ? k_scores_wide<true> : k_scores_wide<false>);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+  const size_t smem = near ? kNearSmem : kWideSmem;
+  const int threads = near ? kThreads : kWideThreads;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   if (fault_hit(kFaultLaunch)) return cudaErrorLaunchFailure;
   count_launch();
-  kern<<<static_cast<unsigned>(grid < nsm ? grid : nsm), kThreads, kSmem, s>>>(*a.xmap, *a.cmap, a.smap ? *a.smap : *a.cmap, k);
+  kern<<<static_cast<unsigned>(grid < nsm ? grid : nsm), threads, smem, s>>>(*a.xmap, *a.cmap, a.smap ? *a.smap : *a.cmap, k);
   return cudaGetLastError();
 }
 

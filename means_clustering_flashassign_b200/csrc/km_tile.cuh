@@ -106,30 +106,31 @@ __device__ __forceinline__ void stage_reusable(int lane) {
 }
 
 // The staged rows, whole lines of 32 in-range rows, to rows of any alignment:
-// words of W bytes (4 or 2) one per lane, a row at a time, eight rows' reads in
-// flight.  Instructions bound this path, not the sectors that rows share
-// (carrying those over from line to line took more).
+// words of W bytes (4 or 2) one per lane, a row at a time.  Three instructions
+// to a row (they bound this path, not the sectors that rows share: carrying
+// those over from line to line took more).
 template <int W>
 __device__ __forceinline__ void store_lines(const uint8_t* stage, uint8_t* dst, uint32_t row_bytes, int lane) {
-  using E = typename std::conditional<W == 2, uint16_t, uint32_t>::type;
 #pragma unroll
   for (int h = 0; h < 4 / W; ++h) {
     const uint32_t o = static_cast<uint32_t>(h * 32 + lane) * W;
-    uint8_t* to = dst + o;
-    uint32_t from[8];  // of the rows k, k + 8, ...
+    uint64_t to = reinterpret_cast<uint64_t>(dst) + o;
 #pragma unroll
-    for (uint32_t k = 0; k < 8; ++k) from[k] = smem_addr(stage) + k * 128 + ((((o >> 4) ^ k) & 7) << 4) + (o & 15);
+    for (uint32_t k = 0; k < 8; ++k) {
+      const uint32_t from = smem_addr(stage) + k * 128 + ((((o >> 4) ^ k) & 7) << 4) + (o & 15);
 #pragma unroll
-    for (uint32_t i = 0; i < 4; ++i) {
-      E v[8];
-#pragma unroll
-      for (uint32_t k = 0; k < 8; ++k) {
-        if constexpr (W == 4) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[k]) : "r"(from[k] + i * 1024));
-        else asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v[k]) : "r"(from[k] + i * 1024));
+      for (uint32_t i = 0; i < 4; ++i) {
+        const uint64_t at = to + static_cast<uint64_t>(i * 8 + k) * row_bytes;
+        if (W == 4) {
+          uint32_t v;
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(from + i * 1024));
+          asm volatile("st.global.b32 [%0], %1;" ::"l"(at), "r"(v) : "memory");
+        } else {
+          uint16_t v;
+          asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(from + i * 1024));
+          asm volatile("st.global.b16 [%0], %1;" ::"l"(at), "h"(v) : "memory");
+        }
       }
-#pragma unroll
-      for (uint32_t k = 0; k < 8; ++k)
-        *reinterpret_cast<E*>(to + static_cast<uint64_t>(i * 8 + k) * row_bytes) = v[k];
     }
   }
 }
@@ -141,16 +142,10 @@ __device__ __forceinline__ void store_ragged(const uint8_t* stage, uint8_t* dst,
   using E = typename std::conditional<ES == 2, uint16_t, uint32_t>::type;
   for (int c = lane; c < n; c += 32) {
     const int o = c * ES;
-#pragma unroll 1
-    for (int r0 = 0; r0 < rows; r0 += 8) {
-      E v[8];
-#pragma unroll
-      for (int r = 0; r < 8; ++r)
-        v[r] = *reinterpret_cast<const E*>(stage + (r0 + r) * 128 + ((((o >> 4) ^ r) & 7) << 4) + (o & 15));
-#pragma unroll
-      for (int r = 0; r < 8; ++r)
-        if (r0 + r < rows) *reinterpret_cast<E*>(dst + (r0 + r) * row_bytes + o) = v[r];
-    }
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r)
+      *reinterpret_cast<E*>(dst + r * row_bytes + o) =
+          *reinterpret_cast<const E*>(stage + r * 128 + ((((o >> 4) ^ r) & 7) << 4) + (o & 15));
   }
 }
 
