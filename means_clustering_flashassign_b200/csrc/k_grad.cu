@@ -33,6 +33,8 @@
 // points, those joined in float64).  The epilogue warps hold a whole dC tile in
 // registers, 128 sums a thread, so the warpgroups divide the launch's registers
 // anew (setmaxnreg).  Every wait is bounded in time.
+#include <atomic>
+
 #include "km_e4m3.cuh"
 #include "km_internal.h"
 #include "km_soft.h"
@@ -633,10 +635,15 @@ cudaError_t grad_t(const GradArgs& a, const GradK& k, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
   if (e != cudaSuccess) return e;
   // The warpgroups can only divide what the launch was given: a build that asks
-  // for fewer registers would wait for the rest for ever.
-  cudaFuncAttributes fa;
-  if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
-  if ((fa.numRegs + 7) / 8 * 8 < kRegsLaunch) return cudaErrorInvalidKernelImage;
+  // for fewer registers would wait for the rest for ever.  (A constant of the
+  // build, looked up once.)
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+    regs.store(fa.numRegs, std::memory_order_relaxed);
+  }
+  if ((regs.load(std::memory_order_relaxed) + 7) / 8 * 8 < kRegsLaunch) return cudaErrorInvalidKernelImage;
   count_launch();
   return launch_chained(kern, dim3(static_cast<unsigned>(k.groups * k.group)), dim3(kThreads), kSmem, s, *a.ds_x, *a.ds_c,
                         *a.cmap, *a.xmap, k);

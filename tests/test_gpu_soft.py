@@ -632,3 +632,23 @@ def test_every_8_bit_value_under_every_kind_of_scale():
     for got in (dX, dC):
         assert torch.isnan(got[:, col]).all()
         assert torch.equal(got[:, ~col].double(), w[:, ~col])
+
+
+def test_scores_captured_first_and_called_after():
+    """The status word that calls without a workspace share is not a graph's memory."""
+    saved = dict(km._status_words)
+    km._status_words.clear()
+    g = gen(28)
+    qx, qc = km.quantize(randn(g, 500, 64)), km.quantize(randn(g, 60, 64))
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out = km.scores(qx, qc)
+    assert not km._status_words
+    graph.replay()
+    ref = km.scores(qx, qc)
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref) and len(km._status_words) == 1
+    del graph, out
+    assert torch.equal(km.scores(qx, qc), ref)
+    km._status_words.update(saved)
