@@ -486,8 +486,8 @@ int km_scores_grad(const void* dS, const uint8_t* xq, const uint8_t* xs, const u
  *           NULL = all valid.
  *   loss    [B] float; 0 when an instance has no valid point.
  *   counts  [B][K] int32: picks per cluster; rows [B] int32: M.
- *   lse, dot [B][N] float: each row's logsumexp and sum_k f_k p_ik (0 and 0
- *           where not valid), which km_balance_grad takes.
+ *   lse, dot [B][N] float: each row's logsumexp and sum_k (K f_k - 1) p_ik (0
+ *           and 0 where not valid), which km_balance_grad takes.
  * N * T < 2^31.  Results are bitwise reproducible.
  */
 int km_balance(const void* S, const int32_t* idx, const uint8_t* valid, int B, int64_t N, int K, int T, int dtype,
@@ -496,7 +496,7 @@ int km_balance(const void* S, const int32_t* idx, const uint8_t* valid, int B, i
 
 /*
  * Gradient of km_balance's loss with respect to S (the counts are constants):
- *   dS[b][i][k] = grad[b] * (K / M) * p_ik * (f_k - dot_i),
+ *   dS[b][i][k] = grad[b] * (1 / M) * p_ik * (K f_k - 1 - dot_i),
  * 0 in rows that are not valid.  S, valid, counts, rows, lse and dot are those
  * of the forward call; grad [B] float is the loss's own gradient (NULL: 1).
  * dS [B][N][K] dtype, 16-byte aligned, must not overlap S.

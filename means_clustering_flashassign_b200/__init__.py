@@ -741,8 +741,8 @@ class Quantized(NamedTuple):
 class Balance(NamedTuple):
     """What balance() returns: the loss float32 [B], the picks per cluster int32
     (K,) or (B, K), and what its gradient needs: the valid points int32 [B], each
-    row's logsumexp and sum of p * share float32 (N,) or (B, N), and the picks
-    per point."""
+    row's logsumexp and sum of p * (K * share - 1) float32 (N,) or (B, N), and the
+    picks per point."""
     loss: torch.Tensor
     counts: torch.Tensor
     rows: torch.Tensor

@@ -2,9 +2,14 @@
 // per cluster, and the gradient.
 //
 // p_i = softmax(S_i) over the K clusters, M the number of valid points, T the
-// picks per point, f_k = counts_k / (M T) the share of the picks cluster k got:
-//   loss = K * sum_k f_k * mean_i p_ik = (K / M) * sum_i r_i,   r_i = sum_k f_k p_ik
-//   dloss/dS_ik = (K / M) * p_ik * (f_k - r_i)
+// picks per point, u_k = K counts_k / (M T) - 1 the excess of cluster k's picks
+// over an even share:
+//   loss = (1 / M) * sum_i (1 + r_i),   r_i = sum_k p_ik u_k
+//   dloss/dS_ik = (1 / M) * p_ik * (u_k - r_i)
+// which is K * sum_k f_k * mean_i p_ik for the shares f_k = counts_k / (M T), and
+// its gradient (K / M) p_ik (f_k - sum_j f_j p_ij).  Taken from the even share, the
+// difference keeps its digits where the clusters are nearly balanced, and is 0
+// where they are.
 // The counts depend on the picks alone, so they are taken first; then one pass
 // over S gives each row's logsumexp and r_i together, the loss needs no column
 // sums, and the gradient is one read and one write of S, with the row's two
@@ -14,8 +19,8 @@
 //
 // Both row passes are bound by HBM once a row costs few enough instructions
 // and shared-memory-pipe cycles.  A group of 1 to 256 threads holds a row in
-// registers (32 elements a thread at most) and, across all its rows, the shares
-// f of its own columns: fetching those again for every row took more load
+// registers (32 elements a thread at most) and, across all its rows, the excess
+// u of its own columns: fetching those again for every row took more load
 // cycles than the row itself (79 % of the load pipe's, at 2.7 TB/s).  Rows
 // wider than 8192 go through the block in pieces, with running maxima.
 #include <cuda_bf16.h>
@@ -242,9 +247,19 @@ __device__ __forceinline__ float max_of(const Raw<BF16, VEC, NC>& r) {
   }
 }
 
-// The shares of this thread's columns.
+// u_k of a cluster's count.
+struct Excess {
+  float K, picks, unit;  // M * T and its inverse
+  __device__ __forceinline__ Excess(int64_t M, int T, int k)
+      : K(static_cast<float>(k)), picks(static_cast<float>(M * T)), unit(M > 0 ? 1.f / static_cast<float>(M * T) : 0.f) {}
+  __device__ __forceinline__ float operator()(int32_t count) const {
+    return fmaf(static_cast<float>(count), K, -picks) * unit;
+  }
+};
+
+// u of this thread's columns.
 template <int V, int LPR, int NC, int E>
-__device__ __forceinline__ void load_shares(const int32_t* counts, int K, int l, float inv, float (&f)[E]) {
+__device__ __forceinline__ void load_excess(const int32_t* counts, int K, int l, const Excess& ex, float (&u)[E]) {
   const bool wide = V % 4 == 0 && reinterpret_cast<uintptr_t>(counts) % 16 == 0;
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
@@ -253,23 +268,18 @@ __device__ __forceinline__ void load_shares(const int32_t* counts, int K, int l,
 #pragma unroll
       for (int i = 0; i < V; i += 4) {
         const int4 n = c0 < K ? __ldcg(reinterpret_cast<const int4*>(counts + c0 + i)) : make_int4(0, 0, 0, 0);
-        f[j * V + i] = static_cast<float>(n.x) * inv;
+        u[j * V + i] = ex(n.x);
         if constexpr (V >= 4) {
-          f[j * V + i + 1] = static_cast<float>(n.y) * inv;
-          f[j * V + i + 2] = static_cast<float>(n.z) * inv;
-          f[j * V + i + 3] = static_cast<float>(n.w) * inv;
+          u[j * V + i + 1] = ex(n.y);
+          u[j * V + i + 2] = ex(n.z);
+          u[j * V + i + 3] = ex(n.w);
         }
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        f[j * V + i] = c0 + i < K ? static_cast<float>(__ldcg(counts + c0 + i)) * inv : 0.f;
+      for (int i = 0; i < V; ++i) u[j * V + i] = c0 + i < K ? ex(__ldcg(counts + c0 + i)) : 0.f;
     }
   }
-}
-
-__device__ __forceinline__ float share_unit(int64_t M, int T) {
-  return M > 0 ? 1.f / (static_cast<float>(M) * static_cast<float>(T)) : 0.f;
 }
 
 // Maximum (or sum) over the LPR threads of a row; above a warp through shared
@@ -320,7 +330,7 @@ __device__ __forceinline__ void finish_loss(const BalK& p, int b, int blk, doubl
     for (int i = threadIdx.x; i < p.nblk; i += 32) v += __ldcg(&p.part[static_cast<int64_t>(b) * p.nblk + i]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (threadIdx.x == 0) p.loss[b] = __ldcg(&p.rows[b]) > 0 ? static_cast<float>(v * p.K / __ldcg(&p.rows[b])) : 0.f;
+    if (threadIdx.x == 0) p.loss[b] = __ldcg(&p.rows[b]) > 0 ? static_cast<float>(v / __ldcg(&p.rows[b])) : 0.f;
   }
 }
 
@@ -328,6 +338,10 @@ __device__ __forceinline__ void finish_loss(const BalK& p, int b, int blk, doubl
 // -inf) has no probabilities, so r = 0.
 struct RowNumbers {
   float lse, r;
+  // the row's term of the loss: the sum of its probabilities, 1 or 0, and r
+  __device__ __forceinline__ double term() const {
+    return (lse == -CUDART_INF_F ? 0.0 : 1.0) + static_cast<double>(r);
+  }
 };
 __device__ __forceinline__ RowNumbers row_numbers(float m, float s, float t) {
   if (s == 0.f) return {-CUDART_INF_F, 0.f};
@@ -342,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, resident(VEC, NC)) k_bal_rows(const 
   const int l = threadIdx.x % LPR;
   pdl_wait();
   float f[E];
-  load_shares<V, LPR, NC, E>(p.counts + static_cast<int64_t>(b) * p.K, p.K, l, share_unit(__ldcg(&p.rows[b]), p.T), f);
+  load_excess<V, LPR, NC, E>(p.counts + static_cast<int64_t>(b) * p.K, p.K, l, Excess(__ldcg(&p.rows[b]), p.T, p.K), f);
   double sum = 0.0;
   const int64_t step = static_cast<int64_t>(p.nblk) * RPB;
   int64_t i = static_cast<int64_t>(blk) * RPB + threadIdx.x / LPR;
@@ -392,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, resident(VEC, NC)) k_bal_rows(const 
       const RowNumbers n = now ? row_numbers(m, s, t) : RowNumbers{0.f, 0.f};
       p.lse[b * p.N + i] = n.lse;
       p.dot[b * p.N + i] = n.r;
-      sum += n.r;
+      if (now) sum += n.term();
     }
   }
   finish_loss(p, b, blk, sum);
@@ -405,9 +419,9 @@ __global__ void __launch_bounds__(kThreads, resident(VEC, NC)) k_bal_grad(const 
   const int b = blockIdx.x / p.nblk, blk = blockIdx.x - b * p.nblk;
   const int l = threadIdx.x % LPR;
   const int64_t M = p.rows[b];
-  const float coef = M > 0 ? (p.grad ? p.grad[b] : 1.f) * static_cast<float>(p.K) / static_cast<float>(M) : 0.f;
+  const float coef = M > 0 ? (p.grad ? p.grad[b] : 1.f) / static_cast<float>(M) : 0.f;
   float f[E];
-  load_shares<V, LPR, NC, E>(p.counts + static_cast<int64_t>(b) * p.K, p.K, l, share_unit(M, p.T), f);
+  load_excess<V, LPR, NC, E>(p.counts + static_cast<int64_t>(b) * p.K, p.K, l, Excess(M, p.T, p.K), f);
 #pragma unroll
   for (int j = 0; j < E; ++j) f[j] *= coef;
   Raw<BF16, VEC, NC> next;
@@ -511,7 +525,7 @@ __global__ void __launch_bounds__(kThreads) k_bal_rows_wide(const elem_t<BF16>* 
   __shared__ float sm[3][kWarps];
   const int b = blockIdx.x / p.nblk, blk = blockIdx.x - b * p.nblk;
   pdl_wait();
-  const float inv = share_unit(__ldcg(&p.rows[b]), p.T);
+  const Excess ex(__ldcg(&p.rows[b]), p.T, p.K);
   const int32_t* cnt = p.counts + static_cast<int64_t>(b) * p.K;
   double sum = 0.0;
   for (int64_t i = blk; i < p.N; i += p.nblk) {
@@ -534,7 +548,7 @@ __global__ void __launch_bounds__(kThreads) k_bal_rows_wide(const elem_t<BF16>* 
           if (j < n) {
             const float e = exp_of(v[j] - sh);
             s += e;
-            t = fmaf(e, static_cast<float>(__ldcg(cnt + c + j)), t);
+            t = fmaf(e, ex(__ldcg(cnt + c + j)), t);
           }
       });
     const float top = row_reduce<kThreads, true>(m, sm[0]);
@@ -543,10 +557,10 @@ __global__ void __launch_bounds__(kThreads) k_bal_rows_wide(const elem_t<BF16>* 
     s = row_reduce<kThreads, false>(s * k, sm[1]);
     t = row_reduce<kThreads, false>(t * k, sm[2]);
     if (threadIdx.x == 0) {
-      const RowNumbers n = on ? row_numbers(top, s, t * inv) : RowNumbers{0.f, 0.f};
+      const RowNumbers n = on ? row_numbers(top, s, t) : RowNumbers{0.f, 0.f};
       p.lse[o] = n.lse;
       p.dot[o] = n.r;
-      sum += n.r;
+      if (on) sum += n.term();
     }
   }
   finish_loss(p, b, blk, sum);
@@ -558,8 +572,8 @@ __global__ void __launch_bounds__(kThreads) k_bal_grad_wide(const elem_t<BF16>* 
   constexpr int V = BF16 ? 8 : 4;
   const int b = blockIdx.x / p.nblk, blk = blockIdx.x - b * p.nblk;
   const int64_t M = p.rows[b];
-  const float inv = share_unit(M, p.T);
-  const float coef = M > 0 ? (p.grad ? p.grad[b] : 1.f) * static_cast<float>(p.K) / static_cast<float>(M) : 0.f;
+  const Excess ex(M, p.T, p.K);
+  const float coef = M > 0 ? (p.grad ? p.grad[b] : 1.f) / static_cast<float>(M) : 0.f;
   const int32_t* cnt = p.counts + static_cast<int64_t>(b) * p.K;
   for (int64_t i = blk; i < p.N; i += p.nblk) {
     const int64_t o = b * p.N + i;
@@ -571,7 +585,7 @@ __global__ void __launch_bounds__(kThreads) k_bal_grad_wide(const elem_t<BF16>* 
 #pragma unroll
       for (int j = 0; j < V; ++j)
         d[j] = on && j < n
-                   ? coef * exp_of(v[j] - ls) * (static_cast<float>(cnt[c + j]) * inv - r) : 0.f;
+                   ? coef * exp_of(v[j] - ls) * (ex(cnt[c + j]) - r) : 0.f;
       if (n == 1) {
         if constexpr (BF16) out[c] = __float2bfloat16_rn(d[0]);
         else out[c] = d[0];

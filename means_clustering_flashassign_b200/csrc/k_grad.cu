@@ -57,7 +57,7 @@ constexpr int kEpiWarps = 8, kSumWarps = 4;
 constexpr int kEpiWarp0 = 4, kSumWarp0 = kEpiWarp0 + kEpiWarps;
 // Slices of one accumulation, at most: dC's are added up in registers, dX's
 // (float32) in memory.
-constexpr int kChainC = 8, kChainX = 16;
+constexpr int kChainC = 8, kChainX = 8;
 // Registers per thread: at launch, and as the warpgroups divide them.
 constexpr int kRegsLaunch = 128, kRegsEpi = 184, kRegsRest = 72;
 static_assert(32 * kEpiWarps * kRegsEpi + (kThreads - 32 * kEpiWarps) * kRegsRest <= kThreads * kRegsLaunch, "registers");
