@@ -73,7 +73,7 @@ struct ScoresK {
   int B, K, nb, D;
   int64_t N;
   int64_t mt, nt;  // tiles per instance
-  int64_t ntiles;
+  int64_t wt;      // k_scores_near: work of a point tile against all centroid tiles, 4 for each whole one
   int64_t runs;    // runs of centroid tiles per instance
   int64_t units;   // k_scores_wide: (instance, point tile, run) triples
   void* S;
@@ -160,8 +160,17 @@ __device__ __forceinline__ float4 load_bias(const ScoresK& p, int b, int n0, int
   return v;
 }
 
+// Chunks of 32 columns that the epilogue takes for ncol of them (whole lines).
+template <bool BF16>
+__host__ __device__ constexpr int chunks_of(int ncol) {
+  return BF16 ? (ncol + 63) / 64 * 2 : (ncol + 31) / 32;
+}
+
 // One accumulator to S: 32 points per warp, the tile's 128 columns in staged
-// lines of 128 bytes; the TMEM loads run one 32-column chunk ahead.
+// lines of 128 bytes.  A chunk of 32 columns is loaded once the one before it is
+// staged, so that its load runs under the stores and no second chunk's
+// registers are held (with them the narrow kernel spills); chunks behind K are
+// skipped.
 template <bool BF16>
 __device__ __forceinline__ void emit_tile(const ScoresK& p, const CUtensorMap* smap, int b, int64_t m, int n0, uint32_t tm,
                                           uint64_t* empty, uint8_t* stage, float* bias, float4 bias4, int lane) {
@@ -170,28 +179,34 @@ __device__ __forceinline__ void emit_tile(const ScoresK& p, const CUtensorMap* s
   const int rows = static_cast<int>(m + 32 <= p.N ? 32 : (p.N > m ? p.N - m : 0));
   const int64_t row_bytes = static_cast<int64_t>(p.K) * ES;
   const int ncol = p.K - n0 < kBN ? p.K - n0 : kBN;
+  const int nch = chunks_of<BF16>(ncol);
   reinterpret_cast<float4*>(bias)[lane] = bias4;
   __syncwarp();
-  uint32_t r[2][32];
-  tmem_load32(tm, r[0]);
-  tmem_wait32(r[0]);
-#pragma unroll
-  for (int c = 0; c < kBN / 32; ++c) {
-    if (c + 1 < kBN / 32) tmem_load32(tm + static_cast<uint32_t>((c + 1) * 32), r[(c + 1) & 1]);
+  uint32_t r[32];
+  tmem_load32(tm, r);
+#pragma unroll 1
+  for (int c = 0; c < nch; ++c) {
+    tmem_wait32(r);
+    if (c + 1 == nch) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty);
+    }
     float v[32];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float4 bv = reinterpret_cast<const float4*>(bias + c * 32)[i];
-      v[4 * i] = fmaf(__uint_as_float(r[c & 1][4 * i]), p.alpha, bv.x);
-      v[4 * i + 1] = fmaf(__uint_as_float(r[c & 1][4 * i + 1]), p.alpha, bv.y);
-      v[4 * i + 2] = fmaf(__uint_as_float(r[c & 1][4 * i + 2]), p.alpha, bv.z);
-      v[4 * i + 3] = fmaf(__uint_as_float(r[c & 1][4 * i + 3]), p.alpha, bv.w);
+      v[4 * i] = fmaf(__uint_as_float(r[4 * i]), p.alpha, bv.x);
+      v[4 * i + 1] = fmaf(__uint_as_float(r[4 * i + 1]), p.alpha, bv.y);
+      v[4 * i + 2] = fmaf(__uint_as_float(r[4 * i + 2]), p.alpha, bv.z);
+      v[4 * i + 3] = fmaf(__uint_as_float(r[4 * i + 3]), p.alpha, bv.w);
     }
     const int c0 = BF16 ? (c & ~1) * 32 : c * 32;  // first column of the staged line
     if (p.boxes && (!BF16 || !(c & 1))) stage_reusable(lane);
     if constexpr (BF16) stage_bf16(stage, v, c & 1, lane);
     else stage_f32(stage, v, lane);
-    if ((!BF16 || (c & 1)) && c0 < ncol) {
+    if (c + 1 < nch) tmem_load32(tm + static_cast<uint32_t>((c + 1) * 32), r);
+    if (!BF16 || (c & 1)) {
       if (p.boxes) {
         if (rows > 0) store_box(stage, smap, n0 + c0, static_cast<int>(m), b, lane);
       } else {
@@ -203,14 +218,6 @@ __device__ __forceinline__ void emit_tile(const ScoresK& p, const CUtensorMap* s
         else if (!BF16 || p.pairs) store_lines<4>(stage, out, static_cast<uint32_t>(row_bytes), lane);
         else store_lines<2>(stage, out, static_cast<uint32_t>(row_bytes), lane);
         __syncwarp();
-      }
-    }
-    if (c + 1 < kBN / 32) {
-      tmem_wait32(r[(c + 1) & 1]);
-      if (c + 2 == kBN / 32) {  // the last chunk is in registers
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty);
       }
     }
   }
@@ -304,8 +311,10 @@ __device__ __forceinline__ void block_mma(uint32_t d, uint32_t a, uint32_t b, in
 // Narrow points: units (instance, run of centroid tiles, point tile), point
 // tiles fastest; a CTA takes consecutive units and reloads the centroids only
 // where the run changes.  Run r of an instance holds its centroid tiles
-// [r nt / runs, (r + 1) nt / runs), and the CTAs' shares are cut by tiles, so
-// that runs of different lengths leave no CTA with more work.
+// [r nt / runs, (r + 1) nt / runs), and the CTAs' shares are cut by work, so
+// that neither runs of different lengths nor a last tile of few columns leave
+// a CTA with more (99,991 x 200 points, fp32, a last tile of 9 columns, K = 777:
+// 164 -> 154..160 us against counting it whole; of 8, K = 776: 95..98 -> 89..91).
 struct UnitPos {
   int b, r, j0, j1;  // instance, run, its centroid tiles
   int64_t m;
@@ -313,14 +322,17 @@ struct UnitPos {
     j0 = static_cast<int>(r * p.nt / p.runs);
     j1 = static_cast<int>((r + 1) * p.nt / p.runs);
   }
-  // the first unit at or behind tile t (units of one run hold j1 - j0 tiles each)
-  __device__ __forceinline__ UnitPos(int64_t t, const ScoresK& p) {
-    const int64_t per = p.mt * p.nt;
-    b = static_cast<int>(t / per);
-    const int64_t in = t - b * per;
-    r = static_cast<int>(((in / p.mt + 1) * p.runs - 1) / p.nt);  // the run that holds tile in / mt
+  // the first unit at or behind work w
+  __device__ __forceinline__ UnitPos(int64_t w, const ScoresK& p) {
+    const int64_t per = p.mt * p.wt;
+    b = static_cast<int>(w / per);
+    const int64_t in = w - b * per;
+    int64_t j = in / (4 * p.mt);  // its centroid tile (only the last one can be of less than 4)
+    if (j >= p.nt) j = p.nt - 1;
+    r = static_cast<int>(((j + 1) * p.runs - 1) / p.nt);  // the run that holds it
     set_run(p);
-    m = (in - j0 * p.mt + (j1 - j0) - 1) / (j1 - j0);
+    const int64_t unit = (j1 == p.nt ? p.wt : 4 * static_cast<int64_t>(j1)) - 4 * static_cast<int64_t>(j0);
+    m = (in - 4 * p.mt * j0 + unit - 1) / unit;
     if (m == p.mt) {
       --m;
       next(p);
@@ -347,7 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nb = p.nb;
   uint8_t* cops = su.ops + 2 * nb * kOpBytes;  // the centroid run, behind two point tiles
-  const UnitPos first(blockIdx.x * p.ntiles / gridDim.x, p), end((blockIdx.x + 1) * p.ntiles / gridDim.x, p);
+  const int64_t work = p.B * p.mt * p.wt;
+  const UnitPos first(blockIdx.x * work / gridDim.x, p), end((blockIdx.x + 1) * work / gridDim.x, p);
   const uint32_t sfb = su.tmem + kSfBase, sfa = sfb + 4 * kNearMaxRun;
 
   if (warp == 0) {
@@ -628,7 +641,6 @@ cudaError_t launch_scores(const ScoresArgs& a, cudaStream_t s) {
   k.N = a.N;
   k.mt = (a.N + kBM - 1) / kBM;
   k.nt = (a.K + kBN - 1) / kBN;
-  k.ntiles = k.mt * k.nt * a.B;
   k.S = a.S;
   k.xwords = k.nb % 4 == 0 && reinterpret_cast<uintptr_t>(a.xs) % 4 == 0;
   k.cwords = k.nb % 4 == 0 && reinterpret_cast<uintptr_t>(a.cs) % 4 == 0;
@@ -642,7 +654,7 @@ cudaError_t launch_scores(const ScoresArgs& a, cudaStream_t s) {
   // Narrow points keep centroid runs in shared memory: two point tiles of nb
   // blocks each leave room for (10 - 2 nb) / nb centroid tiles; shorter runs
   // where the units would not occupy every SM.
-  const bool near = k.nb <= 2;
+  const bool near = k.nb <= 2, bf16 = a.dtype == kDtypeBF16;
   k.runs = (k.nt + kWideRun - 1) / kWideRun;
   k.units = a.B * k.mt * k.runs;
   int64_t grid = k.units;
@@ -652,8 +664,10 @@ cudaError_t launch_scores(const ScoresArgs& a, cudaStream_t s) {
     while (run > 1 && a.B * ((k.nt + run - 1) / run) * k.mt < nsm) --run;
     k.runs = (k.nt + run - 1) / run;
     grid = a.B * k.runs * k.mt;
+    const int last = a.K - static_cast<int>(k.nt - 1) * kBN;
+    const int chunks = bf16 ? chunks_of<true>(last) : chunks_of<false>(last);
+    k.wt = 4 * (k.nt - 1) + (chunks < 2 ? chunks + 2 : 4);  // a tile's waits and MMAs take about two chunks' time
   }
-  const bool bf16 = a.dtype == kDtypeBF16;
   auto kern = near ? (bf16 ? k_scores_near<true> : k_scores_near<false>) : (bf16 ? k_scores_wide<true> : k_scores_wide<false>);
   const size_t smem = near ? kNearSmem : kWideSmem;
   const int threads = near ? kThreads : kWideThreads;

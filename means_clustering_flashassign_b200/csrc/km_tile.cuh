@@ -106,9 +106,11 @@ __device__ __forceinline__ void stage_reusable(int lane) {
 }
 
 // The staged rows, whole lines of 32 in-range rows, to rows of any alignment:
-// words of W bytes (4 or 2) one per lane, a row at a time.  Three instructions
-// to a row (they bound this path, not the sectors that rows share: carrying
-// those over from line to line took more).
+// words of W bytes (4 or 2) one per lane, a row at a time.  A warp's unaligned
+// stores bound this path: an SM gets one away in about 16 cycles, with 21 % of
+// the issue slots, 31 % of L2 and 26 % of HBM in use (99,991 x 777 fp32).
+// Carrying the sectors that rows share over from line to line took longer, and
+// loading eight rows before their stores took as long.
 template <int W>
 __device__ __forceinline__ void store_lines(const uint8_t* stage, uint8_t* dst, uint32_t row_bytes, int lane) {
 #pragma unroll

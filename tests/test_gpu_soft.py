@@ -171,6 +171,19 @@ def test_scores_against_float64(B, N, D, K, dtype):
         assert ((S.double() - ref).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,N,D,K", [(1, 40011, 200, 777), (1, 40011, 40, 129), (3, 9000, 128, 300), (2, 15001, 130, 552),
+                                     (1, 33000, 16, 1128)])
+def test_scores_of_many_points_with_a_short_last_tile(B, N, D, K, dtype):
+    """Shares cut by work: every score is written, whatever the last tile holds."""
+    g = gen(K)
+    X, C = int_points(g, B, N, D), int_points(g, B, K, D)
+    S = torch.full(lead(B, N, K), float("nan"), dtype=dtype, device=DEV)
+    km.scores(km.quantize(X), km.quantize(C), out=S, dtype=dtype)
+    # exact in float32 (as above); bf16 rounds once
+    assert torch.equal(S, (X.double() @ C.double().mT).to(dtype))
+
+
 def test_scores_of_a_block_that_is_not_finite():
     g = gen(5)
     X, C = randn(g, 200, 300), randn(g, 150, 300)
