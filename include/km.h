@@ -497,8 +497,10 @@ int km_balance(const void* S, const int32_t* idx, const uint8_t* valid, int B, i
 /*
  * Gradient of km_balance's loss with respect to S (the counts are constants):
  *   dS[b][i][k] = grad[b] * (1 / M) * p_ik * (K f_k - 1 - dot_i),
- * 0 in rows that are not valid.  S, valid, counts, rows, lse and dot are those
- * of the forward call; grad [B] float is the loss's own gradient (NULL: 1).
+ * 0 in rows that are not valid.  The p_ik have a row's offset taken out: they
+ * are as good far from 0 (a row of nothing but a finite mask value has 1 / K
+ * each) as near it.  S, valid, counts, rows, lse and dot are those of the
+ * forward call; grad [B] float is the loss's own gradient (NULL: 1).
  * dS [B][N][K] dtype, 16-byte aligned, must not overlap S.
  */
 int km_balance_grad(const void* S, const uint8_t* valid, const int32_t* counts, const int32_t* rows, const float* lse,

@@ -1,0 +1,96 @@
+"""The soft-assignment operators over the whole range of their inputs, against
+float64 computations of their definitions: scores far from 0 and masked to
+finite values.
+
+Tolerances count roundings in units of 2^-24 (U), half a float32 step of
+relative error; every one is derived beside its use, row by row."""
+
+import pytest
+import torch
+
+import means_clustering_flashassign_b200 as km
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+U = 2.0 ** -24
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+# ---------------------------------------------- balance far from 0 and masked
+FINE = 16.0   # |logsumexp| up to which one float32 of it is enough
+
+
+def far_rows(g, K, dtype):
+    """Rows of scores as callers have them: with an offset of either sign that
+    the softmax does not see, and rows that a finite mask fills, whole or in
+    part; rows near 0 between them (threads of one warp then differ)."""
+    base = torch.randn(40, K, generator=g, device=DEV)
+    off = torch.tensor([0, 1e3, 0, -1e4, 20, -20, 1e4, 1e6, 0, -1e6], device=DEV).repeat(4)[:, None]
+    S = (base + off).to(dtype)
+    low = torch.finfo(dtype).min
+    S[20], S[21], S[22], S[23], S[24] = low, -1e9, 1e8, -1e4, -1e30
+    S[25] = torch.where(torch.arange(K, device=DEV) % 3 == 1, -float("inf"), low)
+    S[26] = torch.where(torch.arange(K, device=DEV) % 3 == 1, -float("inf"), -1e9)
+    S[27] = -float("inf")
+    S[28, 1:] = low            # one ordinary score
+    S[29] = torch.finfo(dtype).max
+    S[30] = -1e9
+    S[30, K // 2:] = -2e9
+    return S
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("K", [3, 8, 16, 77, 256, 300, 1024, 1500, 1504, 4101, 5000, 8192, 20000])
+def test_balance_gradient_of_rows_far_from_zero(K, dtype):
+    """Every form of the rows: 1 to 256 threads a row, 16-byte and single loads,
+    and the wide one."""
+    g = gen(K)
+    S = far_rows(g, K, dtype)
+    N = S.shape[0]
+    valid = torch.ones(N, dtype=torch.bool, device=DEV)
+    valid[[4, 30, 39]] = False
+    Sv = torch.where(valid[:, None], S, torch.full_like(S, float("nan")))
+    idx = torch.randint(0, K, (N, 2), generator=g, device=DEV, dtype=torch.int32)
+    grad = torch.tensor([0.7], device=DEV)
+    bal = km.balance(Sv, idx, valid=valid)
+    dS = km.balance_grad(Sv, bal, grad=grad, valid=valid)
+    assert not dS[~valid].any() and not dS[27].any()
+
+    M = int(valid.sum())
+    counts = torch.bincount(idx[valid].view(-1).long(), minlength=K)
+    assert torch.equal(bal.counts.long(), counts)
+    s = S.double()
+    m = s.amax(1, keepdim=True).clamp_min(-1e300)        # (the row of -inf)
+    w = torch.exp(s - m)
+    tot = w.sum(1, keepdim=True)
+    p = torch.where(tot > 0, w / tot.clamp_min(1e-300), torch.zeros_like(w))
+    u = K * counts.double() / (2 * M) - 1
+    r = (p * u).sum(1, keepdim=True)
+    coef = float(grad) / M
+    ref = coef * p * (u - r) * valid[:, None]
+    # d = s - logsumexp: float32 rounds the difference and its product with log2 e, whose
+    # constant is rounded too (3 |d|), ex2 is off by 4; the row's sum takes K / 32 + 13 adds of terms
+    # off by that (the mean of |d| under p); what one float32 leaves of the logsumexp shifts d by
+    # at most half a step of it, and not by more than log K
+    lse = torch.where(tot > 0, m + torch.log(tot.clamp_min(1e-300)), torch.zeros_like(m))
+    d = (s - lse).abs().clamp_max(200)                   # (p is 0 in float32 from 104 on)
+    left = (lse.abs() * U).clamp_max(torch.log(torch.tensor(float(K))).item() + 0.1)
+    mean = (p * (d + left)).sum(1, keepdim=True)
+    rel = 3 * (d + left) + 4 + K / 32 + 13 + 3 * mean + 4 + 3 * left + 2
+    # rows near 0 take p = exp(s - lse): its rounding (8 half units of 2^-24 at 16) and logf's (a step of at most 16)
+    rel = (rel + torch.where(lse.abs() <= FINE + 1e-3, 8.0 + 16.0, 0.0)) * U
+    assert float(rel[d < 20].max()) <= (3 * 20 + 35 + 24 + 16 * 3 * 11 + K / 32 + 40) * U   # no tolerance grows with the scores
+    err_r = (p * u.abs() * (rel + (K / 32 + 13) * U)).sum(1, keepdim=True) + 4 * U * r.abs()
+    tol = HALF[dtype] * ref.abs() + coef * p * ((u - r).abs() * (rel + 6 * U) + 4 * U * u.abs() + err_r + 4 * U * r.abs()) + 1e-37
+    err = (dS.double() - ref).abs()
+    assert (err <= tol).all(), (err - tol).max(1).values.argmax()
+    # the loss's own gradient: every row's sums to 0, and the loss itself is the same rows'
+    want = ((p.sum(1) + r[:, 0])[valid]).sum() / M
+    assert (bal.loss[0].double() - want).abs() <= (err_r[valid].sum() / M + 2 ** -20 * (want.abs() + 1))
