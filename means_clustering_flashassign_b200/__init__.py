@@ -805,17 +805,21 @@ def _soft_workspace(op, B, N, D, K, dtype, device, workspace):
 _status_words = {}
 
 
-def _scores_workspace(B, N, D, K, dtype, device, workspace):
+def _scores_workspace(B, N, D, K, dtype, device, raw, workspace):
     """scores() needs a workspace for its status word alone, which nobody reads
-    where the caller brings none: one per device serves all such calls."""
+    where the caller brings none: one for each device and stream serves all such
+    calls.  (Not one for all streams: memory is in order on the stream it was
+    allocated on, and another's call could clear it while work queued there
+    before still uses it.)  A captured call takes its graph's memory, since the
+    graph may be replayed on any stream."""
     if workspace is not None:
         return _soft_workspace(SOFT_SCORES, B, N, D, K, dtype, device, workspace)
     need = soft_workspace_size(SOFT_SCORES, B, N, D, K, dtype)
-    ws = _status_words.get(device.index)
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    ws = _status_words.get((device.index, raw))
     if ws is None or ws.numel() < need:
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-        if not torch.cuda.is_current_stream_capturing():   # a graph's own memory is not kept
-            _status_words[device.index] = ws
+        ws = _status_words[device.index, raw] = torch.empty(need, dtype=torch.uint8, device=device)
     return ws
 
 
@@ -919,7 +923,7 @@ def scores(X: Quantized, C: Quantized, *, bias: Optional[torch.Tensor] = None, a
             out = torch.empty(shp, dtype=dtype, device=dev)
         else:
             _check_tensor(out, "out", dev, dtype, shp)
-        ws = _scores_workspace(B, N, D, K, dt, dev, workspace)
+        ws = _scores_workspace(B, N, D, K, dt, dev, raw, workspace)
         _check(library().km_scores(X.data.data_ptr(), X.scale.data_ptr(), C.data.data_ptr(), C.scale.data_ptr(),
                                    _addr(bias), alpha, B, N, D, K, dt, out.data_ptr(), ws.data_ptr(), ws.numel(), raw))
     return out
