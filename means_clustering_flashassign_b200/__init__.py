@@ -814,12 +814,12 @@ def _scores_workspace(B, N, D, K, dtype, device, raw, workspace):
     graph may be replayed on any stream."""
     if workspace is not None:
         return _soft_workspace(SOFT_SCORES, B, N, D, K, dtype, device, workspace)
-    need = soft_workspace_size(SOFT_SCORES, B, N, D, K, dtype)
-    if torch.cuda.is_current_stream_capturing():
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    ws = _status_words.get((device.index, raw))
-    if ws is None or ws.numel() < need:
-        ws = _status_words[device.index, raw] = torch.empty(need, dtype=torch.uint8, device=device)
+    captured = torch.cuda.is_current_stream_capturing()
+    ws = None if captured else _status_words.get((device.index, raw))
+    if ws is None:   # of one size for every shape
+        ws = torch.empty(soft_workspace_size(SOFT_SCORES, B, N, D, K, dtype), dtype=torch.uint8, device=device)
+        if not captured:
+            _status_words[device.index, raw] = ws
     return ws
 
 
