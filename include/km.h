@@ -464,8 +464,9 @@ int km_scores(const uint8_t* xq, const uint8_t* xs, const uint8_t* cq, const uin
  *   dC    [B][K][D] float    = alpha * dS^T x     (may be NULL)
  *   dbias [B][K] float       = column sums of dS  (may be NULL)
  * A float32 dS enters the tensor cores as three bf16 pieces (24 bits); sums
- * are float32, in a fixed order (bitwise reproducible).  dS must be 16-byte
- * aligned.
+ * are float32, in a fixed order (bitwise reproducible).  An infinity or a NaN
+ * in dS reaches the sums it is a term of, as in float32 arithmetic (an infinity
+ * times a value of 0 is NaN).  dS must be 16-byte aligned.
  */
 int km_scores_grad(const void* dS, const uint8_t* xq, const uint8_t* xs, const uint8_t* cq, const uint8_t* cs,
                    float alpha, int B, int64_t N, int D, int K, int dtype, int dx_dtype, void* dX, float* dC,

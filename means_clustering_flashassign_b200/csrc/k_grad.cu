@@ -573,6 +573,24 @@ __device__ __forceinline__ void prep_copy(const uint32_t* src, uint4* out, int64
   }
 }
 
+// Three bf16 pieces of four float32 of which one has no nearest bf16 but an
+// infinity (from 2^128 - 2^119 on).  They are cut off, 8 bits each, so that no
+// sum of the first ones passes the whole; an infinity or a NaN is its first
+// piece alone, since the next ones would be differences of infinities.
+static __device__ __noinline__ void planes_far(float4 v, __nv_bfloat16* to, int64_t plane) {
+  float x[4] = {v.x, v.y, v.z, v.w};
+  for (int pl = 0; pl < 3; ++pl) {
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      h[i] = x[i] != x[i] ? 0x7fc0u : __float_as_uint(x[i]) >> 16;
+      x[i] -= __uint_as_float(h[i] << 16);
+      if (x[i] != x[i]) x[i] = 0.f;
+    }
+    *reinterpret_cast<uint2*>(to + pl * plane) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+  }
+}
+
 // float32 dS as hi + mid + lo, each piece the bf16 nearest to what is left: 4
 // columns at a time.
 __device__ __forceinline__ void prep_planes(const float* src, __nv_bfloat16* out, int64_t pieces, int64_t rows, int K,
@@ -594,10 +612,19 @@ __device__ __forceinline__ void prep_planes(const float* src, __nv_bfloat16* out
       for (int i = 0; i < 4; ++i)
         if (c + i < K) x[i] = src[row * K + c + i];
     }
+    __nv_bfloat16* to = out + row * ldk + c;
+    constexpr float kTop = 3.3961775e38f;  // 2^128 - 2^119
+    // the largest magnitude as an integer: a NaN's bits are above all others
+    const int top = max(max(__float_as_int(fabsf(x[0])), __float_as_int(fabsf(x[1]))),
+                        max(__float_as_int(fabsf(x[2])), __float_as_int(fabsf(x[3]))));
+    if (top >= __float_as_int(kTop)) {
+      planes_far(make_float4(x[0], x[1], x[2], x[3]), to, rows * ldk);
+      continue;
+    }
 #pragma unroll
     for (int pl = 0; pl < 3; ++pl) {
       const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-      *reinterpret_cast<uint2*>(out + (pl * rows + row) * ldk + c) =
+      *reinterpret_cast<uint2*>(to + pl * rows * ldk) =
           make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
       const float2 fa = __bfloat1622float2(a), fb = __bfloat1622float2(b);
       x[0] -= fa.x, x[1] -= fa.y, x[2] -= fb.x, x[3] -= fb.y;

@@ -94,3 +94,44 @@ def test_balance_gradient_of_rows_far_from_zero(K, dtype):
     # the loss's own gradient: every row's sums to 0, and the loss itself is the same rows'
     want = ((p.sum(1) + r[:, 0])[valid]).sum() / M
     assert (bal.loss[0].double() - want).abs() <= (err_r[valid].sum() / M + 2 ** -20 * (want.abs() + 1))
+
+
+# ------------------------------------------------- float32 dS as bf16 pieces
+def signs(g, *shape):
+    """+-2^-10: exact in 8 bits, products with them exact."""
+    return (torch.randint(0, 2, shape, generator=g, device=DEV) * 2 - 1).float() * 2.0 ** -10
+
+
+@pytest.mark.parametrize("N,D,K", [(300, 64, 90), (257, 130, 64), (70, 16, 33)])
+@pytest.mark.parametrize("v", [3.4e38, -3.4e38, torch.finfo(torch.float32).max, 3.3961775e38, 3.3961773e38,
+                               float("inf"), -float("inf"), float("nan")])
+def test_gradients_of_the_largest_floats_and_of_infinities(N, D, K, v):
+    """One such entry of dS: its row of dX, its row of dC and its dbias are its
+    products (exact: powers of two), every other sum is as without it."""
+    g = gen(K)
+    X, C = signs(g, N, D), signs(g, K, D)
+    dS = torch.zeros(N, K, device=DEV)
+    i, k = N - 2, K - 3
+    dS[i, k] = v
+    dS[i, 0] = dS[0, k] = 3.0
+    dS[1, 1] = 2.0 ** -100
+    dX, dC, db = km.scores_grad(dS, km.quantize(X), km.quantize(C))
+    d = dS.double()
+    for got, ref in ((dX, d @ C.double()), (dC, d.mT @ X.double()), (db, d.sum(0))):
+        # 3 beside 3.4e38 vanishes in float32, in the reference's rounding too
+        assert torch.equal(torch.isnan(got), torch.isnan(ref))
+        assert torch.equal(got.nan_to_num(nan=0.0, posinf=1.0, neginf=-1.0), ref.float().nan_to_num(nan=0.0, posinf=1.0, neginf=-1.0))
+        assert torch.equal(torch.isinf(got), torch.isinf(ref.float()))
+
+
+def test_an_infinity_times_zero_is_not_a_number():
+    X, C = torch.ones(9, 32, device=DEV), torch.ones(20, 32, device=DEV)
+    C[4, 7], X[2, 3] = 0.0, 0.0
+    dS = torch.zeros(9, 20, device=DEV)
+    dS[2, 4] = float("inf")
+    dX, dC, db = km.scores_grad(dS, km.quantize(X), km.quantize(C))
+    assert torch.isnan(dX[2, 7]) and torch.isnan(dC[4, 3]) and db[4] == float("inf")
+    dX[2, 7], dC[4, 3] = float("inf"), float("inf")
+    assert (dX[2] == float("inf")).all() and (dC[4] == float("inf")).all()
+    dX[2], dC[4] = 0.0, 0.0
+    assert not dX.any() and not dC.any()
