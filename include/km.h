@@ -429,7 +429,8 @@ typedef enum km_soft_op {
  * Bytes of workspace the operator needs (0 if the shape is invalid or
  * unsupported; km_last_error() says why).  Never O(N*K), except that
  * KM_SOFT_SCORES_GRAD holds a copy of dS of an odd layout: float32, or K not a
- * multiple of 8.
+ * multiple of 8.  Above 32,768 centroids (10,880 for a float32 dS) it holds
+ * B * N * D floats, for sums that are rounded to bf16 at the end.
  */
 size_t km_soft_workspace_size(int op, int B, int64_t N, int D, int K, int dtype);
 

@@ -58,6 +58,11 @@ constexpr int kEpiWarp0 = 4, kSumWarp0 = kEpiWarp0 + kEpiWarps;
 // Slices of one accumulation, at most: dC's are added up in registers, dX's
 // (float32) in memory.
 constexpr int kChainC = 8, kChainX = 8;
+// Slices of a bf16 dX's one chain, at most: 2048 MMAs lose up to 2^-13 of the
+// result's size, beside the 2^-8 of its rounding.  (K = 2^20 in one chain was
+// 5.4e-3 short on average.)
+constexpr int kChainBf16 = 512;
+static_assert((kChainX & (kChainX - 1)) == 0 && (kChainBf16 & (kChainBf16 - 1)) == 0, "Cursor masks with them");
 // Registers per thread: at launch, and as the warpgroups divide them.
 constexpr int kRegsLaunch = 128, kRegsEpi = 184, kRegsRest = 72;
 static_assert(32 * kEpiWarps * kRegsEpi + (kThreads - 32 * kEpiWarps) * kRegsRest <= kThreads * kRegsLaunch, "registers");
@@ -70,6 +75,7 @@ struct GradK {
   int64_t tpi;         // 256-point tiles per instance
   int nkt, group, passes;  // centroid tiles, CTAs per group, centroid tiles per CTA
   int splits, ndt;
+  int xlast;               // slices of a chain of dX less 1 (a power of two of them)
   int64_t items, groups;
   float alpha;
   void* dX;
@@ -119,7 +125,9 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
 // dealt out between them: each chain is read from tensor memory while the MMAs
 // go on with dX.  A float32 dX's chains of kChainX are added in memory (one
 // thread adds to an element, in order: the result is reproducible); a bf16 dX
-// takes its K terms in one.
+// takes its K terms in one, up to kChainBf16 slices; beyond, chains of as many are
+// added in float32 memory and rounded at the end (4,096 x 128 x 16,384 of a
+// float32 dS: 705 us, one chain 692, chains of kChainX 1,185).
 template <bool WX, bool ROWS, bool XCHAINS>
 struct Cursor {
   const GradK& p;
@@ -185,13 +193,13 @@ struct Cursor {
   }
   // the first and the last slice of a chain
   __device__ __forceinline__ bool opens() const {
-    return x ? i == 0 || (XCHAINS && i % kChainX == 0) : i % kChainC == 0;
+    return x ? i == 0 || (XCHAINS && (i & p.xlast) == 0) : i % kChainC == 0;
   }
   __device__ __forceinline__ bool closes() const {
-    return x ? i == nx - 1 || (XCHAINS && i % kChainX == kChainX - 1) : i + 1 == e;
+    return x ? i == nx - 1 || (XCHAINS && (i & p.xlast) == p.xlast) : i + 1 == e;
   }
   // the chain is its result's first (x: of the tile, else of the item's pass)
-  __device__ __forceinline__ bool first_chain() const { return x ? i < kChainX : t == w.t0 && part == 0; }
+  __device__ __forceinline__ bool first_chain() const { return x ? i <= p.xlast : t == w.t0 && part == 0; }
   // the last point slice of an item's pass
   __device__ __forceinline__ bool ends() const { return !x && i == nc - 1 && t + p.group >= w.t1; }
   __device__ __forceinline__ int plane() const { return p.planes == 1 ? 0 : i % p.planes; }
@@ -512,6 +520,13 @@ __global__ void __launch_bounds__(kT) k_grad_join(const float* cpart, int csplit
   }
 }
 
+// The bf16 dX of sums in float32.
+__global__ void __launch_bounds__(kT) k_grad_round(const float* sums, int64_t n, __nv_bfloat16* __restrict__ dX) {
+  pdl_wait();
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kT + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * kT)
+    dX[i] = __float2bfloat16_rn(__ldcg(sums + i));
+}
+
 struct PrepK {
   GradPrepArgs a;
   unsigned cblocks, xblocks;   // blocks of the centroids' and the points' part
@@ -743,6 +758,7 @@ cudaError_t launch_grad(const GradArgs& a, cudaStream_t s) {
   k.groups = pl.groups < k.items ? pl.groups : k.items;
   k.alpha = a.alpha;
   k.dX = a.dX;
+  k.xlast = (a.rounded_dx ? kChainBf16 : kChainX) - 1;
   k.dC = a.dC;
   k.db = a.db;
   k.status = a.status;
@@ -752,6 +768,13 @@ cudaError_t launch_grad(const GradArgs& a, cudaStream_t s) {
     case 128: return grad_k<128>(a, k, s);
     default: return grad_k<256>(a, k, s);
   }
+}
+
+bool grad_long_dx(int K, int planes) { return static_cast<int64_t>((K + kSlice - 1) / kSlice) * planes > kChainBf16; }
+
+cudaError_t launch_grad_round(const float* sums, int64_t n, void* dX, cudaStream_t s) {
+  count_launch();
+  return launch_chained(k_grad_round, dim3(grid_of(n)), dim3(kT), 0, s, sums, n, static_cast<__nv_bfloat16*>(dX));
 }
 
 cudaError_t launch_grad_join(const float* cpart, int csplits, int64_t nc, float* dC, const float* bpart, int bsplits,

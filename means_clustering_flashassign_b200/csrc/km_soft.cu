@@ -75,7 +75,7 @@ int check_device_once() {
 
 // Workspace layout of an operator (offsets in bytes; the status word is at 0).
 struct Layout {
-  size_t off_cop = 0, off_xop = 0, off_planes = 0, off_parts = 0, off_cols = 0, off_bal = 0, off_done = 0, total = 0;
+  size_t off_cop = 0, off_xop = 0, off_planes = 0, off_dx = 0, off_parts = 0, off_cols = 0, off_bal = 0, off_done = 0, total = 0;
   int planes = 1;
   bool copy_ds = false;
   GradPlan gp{};
@@ -100,6 +100,7 @@ int make_layout(Layout& l, int op, int B, int64_t N, int D, int K, int dtype) {
     l.planes = dtype == KM_F32 ? 3 : 1;
     l.copy_ds = dtype == KM_F32 || K % 8 != 0;  // the tensor maps need rows of 16 bytes
     if (l.copy_ds) l.off_planes = take(static_cast<size_t>(l.planes) * B * N * ceil8(K) * 2);
+    if (grad_long_dx(K, l.planes)) l.off_dx = take(sizeof(float) * static_cast<size_t>(B) * N * D);
     l.gp = grad_plan(B, N, D, K);
     if (l.gp.splits > 1) l.off_parts = take(sizeof(float) * l.gp.splits * static_cast<size_t>(B) * K * D);
     l.off_cols = take(sizeof(float) * l.gp.splits * l.gp.parts * static_cast<size_t>(B) * K);
@@ -278,12 +279,19 @@ int km_scores_grad(const void* dS, const uint8_t* xq, const uint8_t* xs, const u
   a.alpha = alpha;
   a.dx_dtype = dx_dtype;
   a.dX = dX;
+  float* sums = dX && dx_dtype == KM_BF16 && grad_long_dx(K, l.planes) ? reinterpret_cast<float*>(c.ws + l.off_dx) : nullptr;
+  if (sums) {
+    a.dx_dtype = KM_F32;
+    a.dX = sums;
+    a.rounded_dx = true;
+  }
   float* parts = l.gp.splits > 1 ? reinterpret_cast<float*>(c.ws + l.off_parts) : dC;
   a.dC = dC ? parts : nullptr;
   a.db = dbias ? reinterpret_cast<float*>(c.ws + l.off_cols) : nullptr;
   a.status = c.status();
   a.limit_ns = api_wait_limit_ns();
   SOFT_CUDA(launch_grad(a, c.s));
+  if (sums) SOFT_CUDA(launch_grad_round(sums, static_cast<int64_t>(B) * N * D, dX, c.s));
   const int64_t nc = dC && l.gp.splits > 1 ? static_cast<int64_t>(B) * K * D : 0;
   const int64_t nb = dbias ? static_cast<int64_t>(B) * K : 0;
   if (nc + nb) SOFT_CUDA(launch_grad_join(parts, l.gp.splits, nc, dC, a.db, l.gp.splits * l.gp.parts, nb, dbias, c.s));

@@ -79,12 +79,18 @@ struct GradArgs {
   float alpha;
   int dx_dtype;
   void* dX;   // or null
+  bool rounded_dx;  // a float32 dX that launch_grad_round takes to bf16
   float* dC;  // [splits][B][K][D] or null
   float* db;  // [splits * parts][B][K] or null
   unsigned int* status;
   uint64_t limit_ns;
 };
 cudaError_t launch_grad(const GradArgs& a, cudaStream_t s);
+// A bf16 dX of so many slices of 64 terms (times planes) is summed in float32
+// memory, by launch_grad with a float32 dX (rounded_dx), and rounded by
+// launch_grad_round.
+bool grad_long_dx(int K, int planes);
+cudaError_t launch_grad_round(const float* sums, int64_t n, void* dX, cudaStream_t s);
 // dC and dbias as the sums of their pieces, in order (nc or nb 0: left out).
 cudaError_t launch_grad_join(const float* cpart, int csplits, int64_t nc, float* dC, const float* bpart, int bsplits,
                              int64_t nb, float* dbias, cudaStream_t s);

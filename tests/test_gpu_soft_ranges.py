@@ -135,3 +135,31 @@ def test_an_infinity_times_zero_is_not_a_number():
     assert (dX[2] == float("inf")).all() and (dC[4] == float("inf")).all()
     dX[2], dC[4] = 0.0, 0.0
     assert not dX.any() and not dC.any()
+
+
+# ---------------------------------------------------- a bf16 dX of many terms
+@pytest.mark.parametrize("B,N,D,K,dtype", [
+    (1, 70, 136, 1 << 20, torch.bfloat16), (1, 70, 40, 1 << 20, torch.float32), (1, 300, 64, 32768, torch.bfloat16),
+    (1, 300, 65, 32769, torch.bfloat16), (2, 257, 8, 40001, torch.bfloat16), (1, 600, 130, 10880, torch.float32),
+    (3, 100, 24, 10881, torch.float32), (1, 1, 5, 70000, torch.float32)])
+def test_bf16_gradient_of_many_terms(B, N, D, K, dtype):
+    """Terms of one sign, so that what the tensor core cuts off adds up: at most
+    2048 MMAs in one float32 chain, each losing up to 2^-23 of the sum, then one
+    rounding to bf16 (2^-8 at most, of either sign: the mean over all elements
+    falls with their number)."""
+    g = gen(K + N)
+    shape = (B,) if B > 1 else ()
+    qx = km.quantize(torch.rand(*shape, N, D, generator=g, device=DEV))
+    qc = km.quantize(torch.rand(*shape, K, D, generator=g, device=DEV) + 0.5)
+    dS = torch.rand(*shape, N, K, generator=g, device=DEV).to(dtype)
+    dX, dC, db = km.scores_grad(dS, qx, qc, dtype=torch.bfloat16, alpha=0.5)
+    assert dX.dtype == torch.bfloat16
+    c, x = km.dequantize(qc, torch.float32).double(), km.dequantize(qx, torch.float32).double()
+    ref = 0.5 * (dS.double() @ c)
+    err = (dX.double() - ref) / ref
+    assert err.abs().max() <= 2.0 ** -8 + 2048 * 2.0 ** -23
+    assert err.mean().abs() <= 2048 * 2.0 ** -23 + 4 * 2.0 ** -8 / err.numel() ** 0.5
+    # alone, and beside no dC, the same bits; dC and dbias as ever
+    assert torch.equal(km.scores_grad(dS, qx, qc, dtype=torch.bfloat16, alpha=0.5, want_dC=False, want_dbias=False)[0], dX)
+    assert ((dC.double() - 0.5 * dS.double().mT @ x).norm() <= 1e-5 * dC.double().norm())
+    assert (db.double() - dS.double().sum(-2)).norm() <= 1e-6 * db.double().norm()

@@ -173,3 +173,16 @@ def test_chained_kernels_wait_before_they_touch_the_chains_data(kernel):
     for fname, body in bodies:
         w = body.find("pdl_wait();")
         assert w >= 0 and "return;" not in body[:w], (kernel, fname)
+
+
+def test_the_rounding_of_a_long_gradient_waits_and_has_room():
+    """k_grad_round is chained like the kernels above; its sums are a float32 dX of
+    workspace where the terms of an element pass 512 slices of 64, and none below."""
+    import test_chain_rule as rule
+    (_, body), = rule._kernel_bodies("k_grad_round")
+    assert body.find("pdl_wait();") < body.find("sums +")
+    for dtype, last in ((km.BF16, 512 * 64), (km.F32, 170 * 64)):
+        size = [km.soft_workspace_size(km.SOFT_SCORES_GRAD, 2, 50, 72, K, dtype) for K in (last, last + 8)]
+        assert size[1] - size[0] >= 2 * 50 * 72 * 4
+        # and no more beyond it than 8 centroids take: their operand, planes and pieces
+        assert size[1] - size[0] <= 2 * 50 * 72 * 4 + 8 * 2 * (72 * 2 + 3 * 50 * 2 + 148 * 4 * 80) + 4096
