@@ -533,8 +533,9 @@ __global__ void __launch_bounds__(kThreads, resident(VEC, NC)) k_bal_grad(const 
 // ------------------------------------------------------------------ wide rows
 // The row's elements in order, 16 aligned bytes at a time where the row allows
 // it: f(values, first column, how many).  A row of an odd width starts between
-// two 16-byte boundaries; its first and last few elements go one by one.
-template <bool BF16, typename F>
+// two 16-byte boundaries; its first and last few elements go one by one.  U pieces
+// are loaded before the first is used.
+template <bool BF16, int U, typename F>
 __device__ __forceinline__ void for_row(const elem_t<BF16>* row, int K, F&& f) {
   constexpr int V = BF16 ? 8 : 4;
   constexpr int ES = BF16 ? 2 : 4;
@@ -549,22 +550,27 @@ __device__ __forceinline__ void for_row(const elem_t<BF16>* row, int K, F&& f) {
     else v[0] = row[c];
     f(v, c, 1);
   }
-  for (int i = l; i < nv; i += kThreads) {
-    float v[V];
-    const int c = head + i * V;
-    if constexpr (BF16) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + c));
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  for (int i = l; i < nv; i += U * kThreads) {
+    uint4 u[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (i + k * kThreads < nv) u[k] = __ldg(reinterpret_cast<const uint4*>(row + head + (i + k * kThreads) * V));
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (i + k * kThreads >= nv) break;
+      const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+      float v[V];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        v[2 * j] = __uint_as_float(w[j] << 16);
-        v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        if constexpr (BF16) {
+          v[2 * j] = __uint_as_float(w[j] << 16);
+          v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        } else {
+          v[j] = __uint_as_float(w[j]);
+        }
       }
-    } else {
-      const float4 u = __ldg(reinterpret_cast<const float4*>(row + c));
-      v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+      f(v, head + (i + k * kThreads) * V, V);
     }
-    f(v, c, V);
   }
 }
 
@@ -583,7 +589,7 @@ __global__ void __launch_bounds__(kThreads) k_bal_rows_wide(const elem_t<BF16>* 
     const bool on = !p.valid || p.valid[o];
     float m = -CUDART_INF_F, s = 0.f, t = 0.f;
     if (on)
-      for_row<BF16>(S + o * p.K, p.K, [&](const float (&v)[V], int c, int n) {
+      for_row<BF16, 1>(S + o * p.K, p.K, [&](const float (&v)[V], int c, int n) {
         float top = m;
 #pragma unroll
         for (int j = 0; j < V; ++j)
@@ -616,8 +622,15 @@ __global__ void __launch_bounds__(kThreads) k_bal_rows_wide(const elem_t<BF16>* 
   finish_loss(p, b, blk, sum);
 }
 
+// Rows summed again as in k_bal_grad.  That loop beside the other one costs the
+// rows that are not: 410 instead of 362 us for 32,768 x 8192 fp32 in the 32
+// registers of eight blocks per SM.  Two pieces in flight in 64 registers, four
+// blocks, win it back: 355 (16,384 columns of bf16 582 against 597, rows that start
+// between 16-byte boundaries 484 against 477); in 40 or 48 registers it spills or
+// waits (426 to 530).
+constexpr int kWideGradBlocks = 4;
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) k_bal_grad_wide(const elem_t<BF16>* __restrict__ S,
+__global__ void __launch_bounds__(kThreads, kWideGradBlocks) k_bal_grad_wide(const elem_t<BF16>* __restrict__ S,
                                                             elem_t<BF16>* __restrict__ dS, const BalK p) {
   constexpr int V = BF16 ? 8 : 4;
   __shared__ float sm[2][kWarps];
@@ -635,7 +648,7 @@ __global__ void __launch_bounds__(kThreads) k_bal_grad_wide(const elem_t<BF16>* 
     float shift = 0.f;
     if (on && coarse(ls)) {  // as in k_bal_grad
       float s = 0.f;
-      for_row<BF16>(S + o * p.K, p.K, [&](const float (&v)[V], int, int n) {
+      for_row<BF16, 2>(S + o * p.K, p.K, [&](const float (&v)[V], int, int n) {
 #pragma unroll
         for (int j = 0; j < V; ++j)
           if (j < n) s += exp_of(v[j] - ls);
@@ -643,7 +656,7 @@ __global__ void __launch_bounds__(kThreads) k_bal_grad_wide(const elem_t<BF16>* 
       shift = -log2f(row_sum<kThreads>(s, sm[turn]));
       turn ^= 1;
     }
-    for_row<BF16>(S + o * p.K, p.K, [&](const float (&v)[V], int c, int n) {
+    for_row<BF16, 2>(S + o * p.K, p.K, [&](const float (&v)[V], int c, int n) {
       float d[V];
 #pragma unroll
       for (int j = 0; j < V; ++j)
@@ -808,7 +821,7 @@ cudaError_t launch_balance_grad(const BalanceArgs& a, cudaStream_t s) {
   if (a.N == 0) return cudaSuccess;
   BalK k = make_k(a);
   const RowForm r = row_form(a.K, a.dtype);
-  k.nblk = blocks_for(a.B, a.N, r, r.lpr ? resident(r.vec, r.nc) : 8);
+  k.nblk = blocks_for(a.B, a.N, r, r.lpr ? resident(r.vec, r.nc) : kWideGradBlocks);
   return a.dtype == kDtypeBF16 ? grad_launch<true>(a, k, s) : grad_launch<false>(a, k, s);
 }
 
