@@ -247,13 +247,22 @@ __device__ __forceinline__ float max_of(const Raw<BF16, VEC, NC>& r) {
   }
 }
 
-// u_k of a cluster's count.
+// u_k of a cluster's count, (K count - M T) / (M T).  Float32 holds neither a
+// count nor M T (below 2^31) above 2^24, so the even share's whole part is taken
+// off first: K (count - share) - rest, 0 where the picks are even and with the
+// digits of the difference elsewhere.  (The product in 64-bit integers: gradient
+// of 32,768 x 8192 fp32 428 against 363 us.)
 struct Excess {
-  float K, picks, unit;  // M * T and its inverse
-  __device__ __forceinline__ Excess(int64_t M, int T, int k)
-      : K(static_cast<float>(k)), picks(static_cast<float>(M * T)), unit(M > 0 ? 1.f / static_cast<float>(M * T) : 0.f) {}
+  int share;
+  float K, rest, unit;  // unit: 1 / (M T)
+  __device__ __forceinline__ Excess(int64_t M, int T, int k) : K(static_cast<float>(k)) {
+    const uint32_t picks = static_cast<uint32_t>(M * T);
+    share = static_cast<int>(picks / static_cast<uint32_t>(k));
+    rest = static_cast<float>(picks - static_cast<uint32_t>(share) * static_cast<uint32_t>(k));
+    unit = M > 0 ? 1.f / static_cast<float>(picks) : 0.f;
+  }
   __device__ __forceinline__ float operator()(int32_t count) const {
-    return fmaf(static_cast<float>(count), K, -picks) * unit;
+    return fmaf(static_cast<float>(count - share), K, -rest) * unit;
   }
 };
 

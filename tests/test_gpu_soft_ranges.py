@@ -163,3 +163,29 @@ def test_bf16_gradient_of_many_terms(B, N, D, K, dtype):
     assert torch.equal(km.scores_grad(dS, qx, qc, dtype=torch.bfloat16, alpha=0.5, want_dC=False, want_dbias=False)[0], dX)
     assert ((dC.double() - 0.5 * dS.double().mT @ x).norm() <= 1e-5 * dC.double().norm())
     assert (db.double() - dS.double().sum(-2)).norm() <= 1e-6 * db.double().norm()
+
+
+# -------------------------------------------------- counts above float32's 24 bits
+@pytest.mark.parametrize("K,T,count", [(3, 3, (1 << 24) + 1), (77, 1, (1 << 24) + 3), (5000, 128, 386544), (10007, 1024, 174080),
+                                       (2500, 8, 800002)])
+def test_balance_of_even_picks_in_any_number(K, T, count):
+    """Counts as a long accumulation leaves them, given to the gradient: even ones
+    give exactly 0, and one more pick than that is seen (u to 3 roundings)."""
+    g = gen(K)
+    S = torch.randn(6, K, generator=g, device=DEV)
+    M = K * count // T
+    assert M * T == K * count < 1 << 31
+    bal = km.balance(S, torch.zeros(6, dtype=torch.int32, device=DEV))
+    even = bal._replace(counts=torch.full((K,), count, dtype=torch.int32, device=DEV), picks=T,
+                        rows=torch.tensor([M], dtype=torch.int32, device=DEV), dot=torch.zeros(6, device=DEV))
+    dS = km.balance_grad(S, even)
+    assert not dS.any()
+    p = torch.softmax(S.double(), 1)
+    one = even._replace(counts=even.counts.clone())
+    one.counts[1] += 1
+    u = torch.zeros(K, dtype=torch.float64, device=DEV)
+    u[1] = K / (M * T)
+    ref = p * u / M
+    # p: |logsumexp| and |d| below 16, K / 32 + 13 adds of the row's sum (above); u and the products 8
+    tol = ref.abs() * (3 * 16 + 24 + 2 * (K / 32 + 13) + 3 * 16 + 12) * U + 1e-37
+    assert ((km.balance_grad(S, one).double() - ref).abs() <= tol).all()
