@@ -48,6 +48,14 @@ constexpr int kBarBytes = 320;
 // (three 16 KB blocks per 128 coordinates instead of four: L2's bandwidth to
 // the SMs bounds it); stages of one block of each, stages of scales
 constexpr int kWideRun = 2;
+// Blocks of one accumulation of a float32 S, at most; longer rows' chains are added
+// in memory, by the thread that wrote the first, in order.  The tensor core
+// truncates where it adds, which adds up over a chain: 128 MMAs (D = 4096) leave
+// as much as a float32 library product, 512 of them 2.0e-6 and 2,048 3.1e-5 where
+// all terms are of one sign.  (A bf16 S takes all its blocks in one: at most
+// 2^-13 at D = 65,536, beside the 2^-8 of its rounding.)  4096 x 65,536 x 1024: 484 us,
+// 416 in one chain.
+constexpr int kChain = 32;
 constexpr int kStages = 4;
 constexpr int kStageOps = (1 + kWideRun) * kOpBytes;
 constexpr int kSfStages = 8;
@@ -170,8 +178,8 @@ __host__ __device__ constexpr int chunks_of(int ncol) {
 // lines of 128 bytes.  A chunk of 32 columns is loaded once the one before it is
 // staged, so that its load runs under the stores and no second chunk's
 // registers are held (with them the narrow kernel spills); chunks behind K are
-// skipped.
-template <bool BF16>
+// skipped.  ADD: to the sums of the blocks before.
+template <bool BF16, bool ADD = false>
 __device__ __forceinline__ void emit_tile(const ScoresK& p, const CUtensorMap* smap, int b, int64_t m, int n0, uint32_t tm,
                                           uint64_t* empty, uint8_t* stage, float* bias, float4 bias4, int lane) {
   constexpr int ES = BF16 ? 2 : 4;
@@ -202,19 +210,25 @@ __device__ __forceinline__ void emit_tile(const ScoresK& p, const CUtensorMap* s
       v[4 * i + 3] = fmaf(__uint_as_float(r[4 * i + 3]), p.alpha, bv.w);
     }
     const int c0 = BF16 ? (c & ~1) * 32 : c * 32;  // first column of the staged line
-    if (p.boxes && (!BF16 || !(c & 1))) stage_reusable(lane);
+    if constexpr (ADD) stage_landed(lane);
+    else if (p.boxes && (!BF16 || !(c & 1))) stage_reusable(lane);
     if constexpr (BF16) stage_bf16(stage, v, c & 1, lane);
     else stage_f32(stage, v, lane);
     if (c + 1 < nch) tmem_load32(tm + static_cast<uint32_t>((c + 1) * 32), r);
     if (!BF16 || (c & 1)) {
       if (p.boxes) {
-        if (rows > 0) store_box(stage, smap, n0 + c0, static_cast<int>(m), b, lane);
+        if constexpr (ADD) {
+          if (rows > 0) add_box(stage, smap, n0 + c0, static_cast<int>(m), b, lane);
+        } else {
+          if (rows > 0) store_box(stage, smap, n0 + c0, static_cast<int>(m), b, lane);
+        }
       } else {
         __syncwarp();
         const int n = ncol - c0 < kCols ? ncol - c0 : kCols;
         uint8_t* out = static_cast<uint8_t*>(p.S) + (static_cast<int64_t>(b) * p.N + m) * row_bytes +
                        static_cast<int64_t>(n0 + c0) * ES;
-        if (n < kCols || rows < 32) store_ragged<ES>(stage, out, row_bytes, rows, n, lane);
+        if constexpr (ADD) add_ragged(stage, out, row_bytes, rows, n, lane);
+        else if (n < kCols || rows < 32) store_ragged<ES>(stage, out, row_bytes, rows, n, lane);
         else if (!BF16 || p.pairs) store_lines<4>(stage, out, static_cast<uint32_t>(row_bytes), lane);
         else store_lines<2>(stage, out, static_cast<uint32_t>(row_bytes), lane);
         __syncwarp();
@@ -298,14 +312,15 @@ __device__ __forceinline__ void publish_scales(uint64_t* bar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
 }
-// The MMAs of one 128-coordinate block.
-__device__ __forceinline__ void block_mma(uint32_t d, uint32_t a, uint32_t b, int kb, int D, uint32_t sfa, uint32_t sfb) {
+// The MMAs of one 128-coordinate block, the kc-th of its chain.
+__device__ __forceinline__ void block_mma(uint32_t d, uint32_t a, uint32_t b, int kb, int kc, int D, uint32_t sfa,
+                                          uint32_t sfb) {
   const uint32_t id = static_cast<uint32_t>(kb & 3);
   const int left = D - kb * kQBlock;
   const int steps = left >= kQBlock ? 4 : (left + 31) / 32;
   for (int s = 0; s < steps; ++s)
     umma_mx(d, sw128_kmajor_desc(a + s * 32), sw128_kmajor_desc(b + s * 32), mx_idesc(id), sfa, sfb,
-            (kb | s) != 0 ? 1u : 0u);
+            (kc | s) != 0 ? 1u : 0u);
 }
 
 // Narrow points: units (instance, run of centroid tiles, point tile), point
@@ -417,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!mbar_wait(&bars.a_empty[ab], aph ^ 1u, g)) { ok = false; break; }
           tc_fence_after();
           for (int kb = 0; kb < nb; ++kb)
-            block_mma(su.tmem + static_cast<uint32_t>(ab * kBN), a + kb * kOpBytes, c + (j * nb + kb) * kOpBytes, kb, p.D,
+            block_mma(su.tmem + static_cast<uint32_t>(ab * kBN), a + kb * kOpBytes, c + (j * nb + kb) * kOpBytes, kb, kb, p.D,
                       sfa + static_cast<uint32_t>(4 * ss), sfb + static_cast<uint32_t>(4 * j));
           umma_commit(&bars.a_full[ab]);
           if (++ab == kAccs) { ab = 0; aph ^= 1u; }
@@ -486,7 +501,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   scores_teardown(su);
 }
 
-template <bool BF16>
+// CHAINS: in chains of kChain blocks, joined in memory (float32).
+template <bool BF16, bool CHAINS>
 __global__ void __launch_bounds__(kWideThreads, 1)
     k_scores_wide(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap cmap,
              const __grid_constant__ CUtensorMap smap, const ScoresK p) {
@@ -532,16 +548,25 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const int n = tile_pos(t, p).n;
         uint32_t acc[kWideRun];
         int at[kWideRun];
+        auto open = [&]() {
 #pragma unroll
-        for (int j = 0; j < kWideRun; ++j) {
-          if (j >= n) break;
-          if (!mbar_wait(&bars.a_empty[ab], aph ^ 1u, g)) { ok = false; break; }
-          acc[j] = su.tmem + static_cast<uint32_t>(ab * kBN);
-          at[j] = ab;
-          if (++ab == kAccs) { ab = 0; aph ^= 1u; }
-        }
-        if (!ok) break;
+          for (int j = 0; j < kWideRun; ++j) {
+            if (j >= n) break;
+            if (!mbar_wait(&bars.a_empty[ab], aph ^ 1u, g)) { ok = false; break; }
+            acc[j] = su.tmem + static_cast<uint32_t>(ab * kBN);
+            at[j] = ab;
+            if (++ab == kAccs) { ab = 0; aph ^= 1u; }
+          }
+          return ok;
+        };
+        auto close = [&]() {
+#pragma unroll
+          for (int j = 0; j < kWideRun; ++j)
+            if (j < n) umma_commit(&bars.a_full[at[j]]);
+        };
+        if (!CHAINS && !open()) break;
         for (int kb = 0; kb < nb; ++kb) {
+          if (CHAINS && kb % kChain == 0 && !open()) break;
           if ((kb & 3) == 0 && !mbar_wait(&bars.sf_full[ss], sph, g)) { ok = false; break; }
           if (!mbar_wait(&bars.full[st], ph, g)) { ok = false; break; }
           tc_fence_after();
@@ -549,18 +574,19 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           const uint32_t sf = su.tmem + kSfBase + static_cast<uint32_t>(ss * kSfCols);
 #pragma unroll
           for (int j = 0; j < kWideRun; ++j)
-            if (j < n) block_mma(acc[j], a, a + (1 + j) * kOpBytes, kb, p.D, sf, sf + static_cast<uint32_t>(4 * (1 + j)));
+            if (j < n)
+              block_mma(acc[j], a, a + (1 + j) * kOpBytes, kb, CHAINS ? kb % kChain : kb, p.D, sf,
+                        sf + static_cast<uint32_t>(4 * (1 + j)));
           umma_commit(&bars.empty[st]);
           if (++st == kStages) { st = 0; ph ^= 1u; }
           if ((kb & 3) == 3 || kb == nb - 1) {
             umma_commit(&bars.sf_empty[ss]);
             if (++ss == kSfStages) { ss = 0; sph ^= 1u; }
           }
+          if (CHAINS && kb % kChain == kChain - 1 && kb + 1 < nb) close();
         }
         if (!ok) break;
-#pragma unroll
-        for (int j = 0; j < kWideRun; ++j)
-          if (j < n) umma_commit(&bars.a_full[at[j]]);
+        close();
       }
       umma_commit(&bars.drain);  // every MMA is done before TMEM can be released
       settle(&bars.drain, 0u, g);
@@ -618,6 +644,17 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                         bias, bias4, lane);
         if (++ab == kAccs) { ab = 0; aph ^= 1u; }
       }
+      if constexpr (CHAINS) {
+        for (int k0 = kChain; ok && k0 < nb; k0 += kChain) {
+          for (int j = 0; j < tp.n; ++j) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars.a_full[ab], aph, g))) { ok = false; break; }
+            tc_fence_after();
+            emit_tile<BF16, true>(p, &smap, tp.b, tp.m0 + q4 * 32, tp.n0 + j * kBN, tm + static_cast<uint32_t>(ab * kBN),
+                                  &bars.a_empty[ab], stage, bias, make_float4(0.f, 0.f, 0.f, 0.f), lane);
+            if (++ab == kAccs) { ab = 0; aph ^= 1u; }
+          }
+        }
+      }
     }
     stage_reusable(lane);
   }
@@ -668,7 +705,8 @@ cudaError_t launch_scores(const ScoresArgs& a, cudaStream_t s) {
     const int chunks = bf16 ? chunks_of<true>(last) : chunks_of<false>(last);
     k.wt = 4 * (k.nt - 1) + (chunks < 2 ? chunks + 2 : 4);  // a tile's waits and MMAs take about two chunks' time
   }
-  auto kern = near ? (bf16 ? k_scores_near<true> : k_scores_near<false>) : (bf16 ? k_scores_wide<true> : k_scores_wide<false>);
+  auto kern = near ? (bf16 ? k_scores_near<true> : k_scores_near<false>)
+                   : (bf16 ? k_scores_wide<true, false> : (k.nb > kChain ? k_scores_wide<false, true> : k_scores_wide<false, false>));
   const size_t smem = near ? kNearSmem : kWideSmem;
   const int threads = near ? kThreads : kWideThreads;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));

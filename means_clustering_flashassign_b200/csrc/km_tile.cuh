@@ -88,7 +88,8 @@ __device__ __forceinline__ void stage_bf16(uint8_t* stage, const float (&v)[32],
 
 // The warp's staged 32 x 128-byte box to (x, y, z) of a tensor map with that
 // box (rows and columns out of range are not written).  stage_reusable waits
-// until such a store has read the staging rows.
+// until such a store has read the staging rows, stage_landed until it is in
+// memory: two to the same place are in no order by themselves.
 __device__ __forceinline__ void store_box(const uint8_t* stage, const CUtensorMap* map, int x, int y, int z, int lane) {
   fence_proxy_async_smem();
   __syncwarp();
@@ -103,6 +104,22 @@ __device__ __forceinline__ void store_box(const uint8_t* stage, const CUtensorMa
 __device__ __forceinline__ void stage_reusable(int lane) {
   if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   __syncwarp();
+}
+__device__ __forceinline__ void stage_landed(int lane) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  __syncwarp();
+}
+// The box added to what is there (float32).
+__device__ __forceinline__ void add_box(const uint8_t* stage, const CUtensorMap* map, int x, int y, int z, int lane) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(smem_addr(stage))
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
 }
 
 // The staged rows, whole lines of 32 in-range rows, to rows of any alignment:
@@ -148,6 +165,19 @@ __device__ __forceinline__ void store_ragged(const uint8_t* stage, uint8_t* dst,
     for (int r = 0; r < rows; ++r)
       *reinterpret_cast<E*>(dst + r * row_bytes + o) =
           *reinterpret_cast<const E*>(stage + r * 128 + ((((o >> 4) ^ r) & 7) << 4) + (o & 15));
+  }
+}
+
+// store_ragged of float32, added to what is there: the lane that stored an element
+// adds to it.
+__device__ __forceinline__ void add_ragged(const uint8_t* stage, uint8_t* dst, int64_t row_bytes, int rows, int n, int lane) {
+  for (int c = lane; c < n; c += 32) {
+    const int o = c * 4;
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r)
+      asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(dst + r * row_bytes + o)),
+                   "f"(*reinterpret_cast<const float*>(stage + r * 128 + ((((o >> 4) ^ r) & 7) << 4) + (o & 15)))
+                   : "memory");
   }
 }
 

@@ -189,3 +189,34 @@ def test_balance_of_even_picks_in_any_number(K, T, count):
     # p: |logsumexp| and |d| below 16, K / 32 + 13 adds of the row's sum (above); u and the products 8
     tol = ref.abs() * (3 * 16 + 24 + 2 * (K / 32 + 13) + 3 * 16 + 12) * U + 1e-37
     assert ((km.balance_grad(S, one).double() - ref).abs() <= tol).all()
+
+
+# ------------------------------------------------------- scores of long points
+@pytest.mark.parametrize("N,D,K", [(300, 65536, 200), (130, 65536, 77), (33, 8192, 129), (257, 4097, 64), (1, 20000, 5), (150, 12289, 131)])
+def test_scores_of_long_points(N, D, K):
+    """Terms of one sign: a chain of at most 128 MMAs, each cutting off up to 2^-23
+    of a sum that grows evenly (64 of them in effect), the D / 4096 chains added
+    with half a step each, and the result's two roundings."""
+    g = gen(D + K)
+    qx, qc = (km.quantize(torch.rand(n, D, generator=g, device=DEV) + 0.1) for n in (N, K))
+    x, c = (km.dequantize(q, torch.float32).double() for q in (qx, qc))
+    bias = torch.randn(K, generator=g, device=DEV)
+    ref = 0.5 * (x @ c.T) + bias.double()
+    S = km.scores(qx, qc, alpha=0.5, bias=bias)
+    rel = 65 * 2 * U + (D / 4096 + 3) * U
+    assert ((S.double() - ref).abs() <= rel * (ref.abs() + bias.abs())).all()
+    assert torch.equal(km.scores(qx, qc, alpha=0.5, bias=bias), S)
+    # a bf16 result takes one chain: D / 32 of them, half of which count, beside its rounding
+    S16 = km.scores(qx, qc, alpha=0.5, bias=bias, dtype=torch.bfloat16)
+    assert ((S16.double() - ref).abs() <= (HALF[torch.bfloat16] + D / 32 * U + 3 * U) * (ref.abs() + bias.abs())).all()
+
+
+@pytest.mark.parametrize("N,D,K", [(300, 65536, 200), (130, 65536, 77), (33, 8192, 129), (257, 4097, 64), (70, 12300, 260), (3, 40000, 2)])
+def test_scores_of_long_points_of_small_integers_are_exact(N, D, K):
+    g = gen(D + K + 1)
+    X, C = (torch.randint(-1, 2, (n, D), generator=g, device=DEV).float() for n in (N, K))
+    bias = torch.randint(-5, 6, (K,), generator=g, device=DEV).float()
+    buf = torch.full((N + 16, K), 7.0, device=DEV)
+    S = km.scores(km.quantize(X), km.quantize(C), bias=bias, alpha=2.0, out=buf[8:8 + N])
+    assert torch.equal(S.double(), 2 * X.double() @ C.double().T + bias.double())
+    assert (buf[:8] == 7).all() and (buf[8 + N:] == 7).all()
