@@ -407,7 +407,7 @@ int km_plan_describe(int op, int B, int64_t N, int D, int K, int dtype, int64_t 
  *
  * These calls share the conventions at the top of this file, except:
  *  - shapes: 1 <= B <= 65536, 0 <= N < 2^31 (no points: sums are 0),
- *    1 <= D <= 65536, 1 <= K <= 2^20, any D and K (no multiple of 8, and K
+ *    B * N < 2^37, 1 <= D <= 65536, 1 <= K <= 2^20, any D and K (no multiple of 8, and K
  *    may exceed N);
  *  - infinities and NaN have the meaning each call gives.
  *

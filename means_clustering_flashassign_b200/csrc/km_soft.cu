@@ -45,8 +45,9 @@ constexpr int kMaxD = 1 << 16;
 constexpr int kMaxK = 1 << 20;
 constexpr int kMaxT = 1 << 10;
 
-// Shapes shared by all operators: B >= 1 instances, 0 <= N < 2^31 points
-// (B * N < 2^31 * 64, so that grids and tile counts stay in range).
+// Shapes shared by all operators: B >= 1 instances, 0 <= N < 2^31 points, B * N <
+// 2^37 (no GPU holds as many; the sizes and offsets of a workspace, which grow
+// with B N K and B N D, then fit 64 bits).
 int check_shape(int B, int64_t N, int D, int K, int dtype) {
   if (dtype != KM_F32 && dtype != KM_BF16) return sfail(KM_ERR_INVALID_ARG, "unknown dtype %d", dtype);
   if (B < 1 || N < 0 || D < 1 || K < 1)
@@ -54,6 +55,8 @@ int check_shape(int B, int64_t N, int D, int K, int dtype) {
                  static_cast<long long>(N), D, K);
   if (N >= (int64_t(1) << 31)) return sfail(KM_ERR_UNSUPPORTED, "N=%lld must be below 2^31", static_cast<long long>(N));
   if (B > (1 << 16)) return sfail(KM_ERR_UNSUPPORTED, "B=%d above 2^16", B);
+  if (B * N >= (int64_t(1) << 37))
+    return sfail(KM_ERR_UNSUPPORTED, "B * N = %lld must be below 2^37", static_cast<long long>(B * N));
   if (D > kMaxD) return sfail(KM_ERR_UNSUPPORTED, "D=%d above 2^16", D);
   if (K > kMaxK) return sfail(KM_ERR_UNSUPPORTED, "K=%d above 2^20", K);
   return KM_OK;

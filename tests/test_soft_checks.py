@@ -186,3 +186,21 @@ def test_the_rounding_of_a_long_gradient_waits_and_has_room():
         assert size[1] - size[0] >= 2 * 50 * 72 * 4
         # and no more beyond it than 8 centroids take: their operand, planes and pieces
         assert size[1] - size[0] <= 2 * 50 * 72 * 4 + 8 * 2 * (72 * 2 + 3 * 50 * 2 + 148 * 4 * 80) + 4096
+
+
+@pytest.mark.parametrize("B,N,D,K,dtype", [(65536, BIG - 1, 65536, 1 << 20, km.F32), (65536, BIG - 1, 65536, 1, km.BF16),
+                                           (65536, BIG - 1, 1, 1 << 20, km.F32), (64, BIG - 1, 65536, 1 << 20, km.F32),
+                                           (63, BIG - 1, 65536, 1 << 20, km.F32), (65536, (1 << 21) - 1, 65536, 1 << 20, km.F32),
+                                           (65536, 1 << 21, 8, 8, km.BF16)])
+def test_workspace_sizes_do_not_wrap(B, N, D, K, dtype):
+    """No size, or one that holds the operands it stands for (in whole numbers of any length)."""
+    ldd, ldk = (D + 7) // 8 * 8, (K + 7) // 8 * 8
+    least = 2 * B * (N + K) * ldd + (6 * B * N * ldk if dtype == km.F32 else 0)
+    got = km.library().km_soft_workspace_size(km.SOFT_SCORES_GRAD, B, N, D, K, dtype)
+    assert got == 0 if B * N >= 1 << 37 else got >= least
+    L = km.library()
+    buf = (ctypes.c_uint8 * 512)()
+    p = ctypes.c_void_p((ctypes.addressof(buf) + 255) // 256 * 256)
+    if B * N >= 1 << 37:   # and no call of such a shape
+        assert L.km_quantize(p, B, N, D, dtype, p, p, None) == 2
+        assert L.km_scores(p, p, p, p, None, 1.0, B, N, D, K, dtype, p, p, 256, None) == 2
