@@ -1017,8 +1017,8 @@ def balance_grad(S: torch.Tensor, bal: Balance, *, grad: Optional[torch.Tensor] 
             out = torch.empty_like(S)
         else:
             _check_tensor(out, "out", dev, S.dtype, S.shape)
-            if out.numel() and out.data_ptr() == S.data_ptr():
-                raise ValueError("out must not be S")
+            if out.numel() and abs(out.data_ptr() - S.data_ptr()) < S.numel() * S.element_size():
+                raise ValueError("out must not overlap S")
         _check(library().km_balance_grad(S.data_ptr(), _addr(valid), bal.counts.data_ptr(), bal.rows.data_ptr(),
                                          bal.lse.data_ptr(), bal.dot.data_ptr(), _addr(grad), B, N, K, bal.picks, dt,
                                          out.data_ptr(), raw))

@@ -350,6 +350,9 @@ int km_balance_grad(const void* S, const uint8_t* valid, const int32_t* counts, 
     return sfail(KM_ERR_INVALID_ARG, "counts, rows, lse, dot and grad must be 4-byte aligned");
   int r = check_shape(B, N, 1, K, dtype);
   if (r != KM_OK) return r;
+  const uintptr_t bytes = static_cast<uintptr_t>(B) * N * K * (dtype == KM_BF16 ? 2 : 4);
+  const uintptr_t s0 = reinterpret_cast<uintptr_t>(S), d0 = reinterpret_cast<uintptr_t>(dS);
+  if (s0 < d0 + bytes && d0 < s0 + bytes) return sfail(KM_ERR_INVALID_ARG, "dS must not overlap S");
   if ((r = check_device_once()) != KM_OK) return r;
   BalanceArgs a{};
   a.S = S;

@@ -204,3 +204,19 @@ def test_workspace_sizes_do_not_wrap(B, N, D, K, dtype):
     if B * N >= 1 << 37:   # and no call of such a shape
         assert L.km_quantize(p, B, N, D, dtype, p, p, None) == 2
         assert L.km_scores(p, p, p, p, None, 1.0, B, N, D, K, dtype, p, p, 256, None) == 2
+
+
+@pytest.mark.parametrize("dtype,es", [(km.F32, 4), (km.BF16, 2)])
+def test_a_balance_gradient_over_its_own_scores_is_refused(dtype, es):
+    """Rows are read ahead of the rows written: dS anywhere on S would change what
+    later rows are taken from."""
+    L = km.library()
+    buf = (ctypes.c_uint8 * 8192)()
+    a = (ctypes.addressof(buf) + 255) // 256 * 256
+    size = 2 * 20 * 16 * es                # B = 2, N = 20, K = 16
+    call = lambda s, ds: L.km_balance_grad(ctypes.c_void_p(s), None, a, a, a, a, None, 2, 20, 16, 1, dtype, ctypes.c_void_p(ds), None)  # noqa: E731
+    for off in (0, 16, 16 * es, size - 16):
+        assert call(a, a + off) == 1 and call(a + off, a) == 1
+        assert b"overlap" in L.km_last_error()
+    if not torch.cuda.is_available():      # side by side they get as far as the device
+        assert call(a, a + size) == 3 and call(a + size, a) == 3
