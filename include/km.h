@@ -449,10 +449,13 @@ int km_dequantize(const uint8_t* q, const uint8_t* scale, int B, int64_t N, int 
 /*
  * Scores of every point against every centroid, both in 8 bits:
  *   S[b][i][k] = bias[b][k] + alpha * sum_d x[b][i][d] * c[b][k][d]
- * on the tensor cores with float32 sums.  alpha = 2 / t and bias = -|c|^2 / t
- * give the logits of softmax(-|x - c|^2 / t).
+ * on the tensor cores with float32 sums (a float32 S above D = 4096: in chains of
+ * 4096 coordinates, joined in order).  alpha = 2 / t and bias = -|c|^2 / t give the
+ * logits of softmax(-|x - c|^2 / t).
  *   bias  [B][K] float, device; may be NULL.
- *   S     [B][N][K] dtype, device, written (rounded once).
+ *   S     [B][N][K] dtype, device, written (rounded once; a float32 S of several
+ *         chains once for each).  On a boundary of its elements; km_balance and
+ *         km_scores_grad take S and dS on 16-byte boundaries only.
  */
 int km_scores(const uint8_t* xq, const uint8_t* xs, const uint8_t* cq, const uint8_t* cs, const float* bias,
               float alpha, int B, int64_t N, int D, int K, int dtype, void* S, void* workspace,
@@ -490,7 +493,7 @@ int km_scores_grad(const void* dS, const uint8_t* xq, const uint8_t* xs, const u
  *   counts  [B][K] int32: picks per cluster; rows [B] int32: M.
  *   lse, dot [B][N] float: each row's logsumexp and sum_k (K f_k - 1) p_ik (0
  *           and 0 where not valid), which km_balance_grad takes.
- * N * T < 2^31.  Results are bitwise reproducible.
+ * 1 <= T <= 1024 and N * T < 2^31.  Results are bitwise reproducible.
  */
 int km_balance(const void* S, const int32_t* idx, const uint8_t* valid, int B, int64_t N, int K, int T, int dtype,
                float* loss, int32_t* counts, int32_t* rows, float* lse, float* dot, void* workspace,

@@ -912,7 +912,8 @@ def scores(X: Quantized, C: Quantized, *, bias: Optional[torch.Tensor] = None, a
     """Scores of 8-bit points against 8-bit centroids: bias + alpha * x . c for
     every pair, (N, K) or (B, N, K) in `dtype` (bf16 or f32).  bias float32 (K,)
     or (B, K).  alpha = 2 / t and bias = -|c|^2 / t give the logits of a soft
-    assignment by distance."""
+    assignment by distance.  As with assign(), workspace_status() of a workspace
+    passed in tells of an in-kernel wait that ran out."""
     B, N, D, K, batched, dev = _score_args(X, C)
     dt = _soft_dtype(dtype)
     shp = (B, N, K) if batched else (N, K)
@@ -933,7 +934,8 @@ def scores_grad(dS: torch.Tensor, X: Quantized, C: Quantized, *, alpha: float = 
                 dtype: Optional[torch.dtype] = None, want_dX: bool = True, want_dC: bool = True,
                 want_dbias: bool = True, workspace=None, stream=None):
     """Gradients of scores() for the gradient dS (bf16 or f32) of its result,
-    with respect to the values the 8-bit X and C stand for.
+    with respect to the values the 8-bit X and C stand for.  dS starts on a
+    16-byte boundary, as a tensor of its own does (a view of an odd offset may not).
 
     Returns (dX in `dtype`, by default dS's, dC float32, dbias float32), None for
     those not wanted."""
@@ -970,7 +972,8 @@ def balance(S: torch.Tensor, idx: torch.Tensor, *, valid: Optional[torch.Tensor]
     """Balance loss of the soft assignment softmax(S) under the picks idx, and
     the picks per cluster.  S (N, K) or (B, N, K) bf16/f32; idx int32 (N,) or
     (B, N), or with T picks per point (N, T) or (B, N, T); valid (N,) or (B, N)
-    bool: the points that count.  See km_balance."""
+    bool: the points that count.  S starts on a 16-byte boundary, as a tensor of its
+    own does; at most 1024 picks per point.  See km_balance."""
     _contig_cuda(S, "S")
     B, N, K, batched = _shape3(S, "S")
     dt = _dtype_code(S)

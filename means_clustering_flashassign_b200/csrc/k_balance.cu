@@ -13,16 +13,18 @@
 // The counts depend on the picks alone, so they are taken first; then one pass
 // over S gives each row's logsumexp and r_i together, the loss needs no column
 // sums, and the gradient is one read and one write of S, with the row's two
-// numbers.  Softmax sums, r_i and the loss's terms are float32, the loss's sum
+// numbers (a row far from 0 is summed again: coarse, below).  Softmax sums, r_i and the loss's terms are float32, the loss's sum
 // over the rows float64 in a fixed order; counts are integers (any order of
 // the adds gives the same ones).
 //
 // Both row passes are bound by HBM once a row costs few enough instructions
 // and shared-memory-pipe cycles.  A group of 1 to 256 threads holds a row in
-// registers (32 elements a thread at most) and, across all its rows, the excess
-// u of its own columns: fetching those again for every row took more load
-// cycles than the row itself (79 % of the load pipe's, at 2.7 TB/s).  Rows
-// wider than 8192 go through the block in pieces, with running maxima.
+// registers and, across all its rows, the excess u of its own columns: fetching
+// those again for every row took more load cycles than the row itself (79 % of
+// the load pipe's, at 2.7 TB/s).  A thread has four 16-byte pieces where rows
+// are whole numbers of them (up to 8192 columns of bf16, 4096 of float32), else
+// up to 32 single elements (8192 columns).  Wider rows go through the block in
+// pieces, with running maxima.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 

@@ -45,8 +45,7 @@ constexpr uint32_t kSfBase = kAccs * kBN;
 constexpr int kEpiBytes = kStageBytes + kBN * 4;  // per warp: staging rows, and (behind all of those) the tile's bias
 constexpr int kBarBytes = 320;
 // k_scores_wide: a CTA takes a point tile against two centroid tiles at once
-// (three 16 KB blocks per 128 coordinates instead of four: L2's bandwidth to
-// the SMs bounds it); stages of one block of each, stages of scales
+// (three 16 KB blocks per 128 coordinates from L2 instead of four); stages of one block of each, stages of scales
 constexpr int kWideRun = 2;
 // Blocks of one accumulation of a float32 S, at most; longer rows' chains are added
 // in memory, by the thread that wrote the first, in order.  The tensor core
