@@ -96,6 +96,26 @@ def test_balance_gradient_of_rows_far_from_zero(K, dtype):
     assert (bal.loss[0].double() - want).abs() <= (err_r[valid].sum() / M + 2 ** -20 * (want.abs() + 1))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("K", [8, 77, 300, 1024, 1504, 4101, 8192, 20000])
+def test_balance_gradient_of_many_rows_far_from_zero(K, dtype):
+    """The same 40 rows 60 times over, each time the same gradient bit for bit,
+    whichever threads take them and whatever rows they took before."""
+    g = gen(K + 1)
+    S = far_rows(g, K, dtype).repeat(60, 1)
+    idx = torch.randint(0, K, (S.shape[0],), generator=g, device=DEV, dtype=torch.int32)
+    bal = km.balance(S, idx)
+    dS = km.balance_grad(S, bal).view(60, 40, K)
+    assert torch.isfinite(dS).all() and (dS[0, 20] != 0).any()
+    assert torch.equal(dS, dS[:1].expand(60, 40, K).contiguous())
+    # a row's gradient sums to 0: p is off by (K / 32 + 250) U at most (above: |d| of the probable
+    # clusters below 40) and r by as much of its terms; where one cluster has all of the row, u - r
+    # cancels and leaves the rounding of both, of size up to 32 here, over M
+    if dtype == torch.float32:
+        scale = dS.double().abs().sum(-1)
+        assert (dS.double().sum(-1).abs() <= scale * (K / 32 + 250) * 2 * U + 2.0 ** -18 / S.shape[0]).all()
+
+
 # ------------------------------------------------- float32 dS as bf16 pieces
 def signs(g, *shape):
     """+-2^-10: exact in 8 bits, products with them exact."""
@@ -141,7 +161,7 @@ def test_an_infinity_times_zero_is_not_a_number():
 @pytest.mark.parametrize("B,N,D,K,dtype", [
     (1, 70, 136, 1 << 20, torch.bfloat16), (1, 70, 40, 1 << 20, torch.float32), (1, 300, 64, 32768, torch.bfloat16),
     (1, 300, 65, 32769, torch.bfloat16), (2, 257, 8, 40001, torch.bfloat16), (1, 600, 130, 10880, torch.float32),
-    (3, 100, 24, 10881, torch.float32), (1, 1, 5, 70000, torch.float32)])
+    (3, 100, 24, 10881, torch.float32), (1, 1, 5, 70000, torch.float32), (1, 4000, 130, 33000, torch.bfloat16)])
 def test_bf16_gradient_of_many_terms(B, N, D, K, dtype):
     """Terms of one sign, so that what the tensor core cuts off adds up: at most
     2048 MMAs in one float32 chain, each losing up to 2^-23 of the sum, then one
@@ -211,7 +231,8 @@ def test_scores_of_long_points(N, D, K):
     assert ((S16.double() - ref).abs() <= (HALF[torch.bfloat16] + D / 32 * U + 3 * U) * (ref.abs() + bias.abs())).all()
 
 
-@pytest.mark.parametrize("N,D,K", [(300, 65536, 200), (130, 65536, 77), (33, 8192, 129), (257, 4097, 64), (70, 12300, 260), (3, 40000, 2)])
+@pytest.mark.parametrize("N,D,K", [(300, 65536, 200), (130, 65536, 77), (33, 8192, 129), (257, 4097, 64), (70, 12300, 260), (3, 40000, 2),
+                                   (9000, 8192, 1100), (5000, 4100, 1301)])
 def test_scores_of_long_points_of_small_integers_are_exact(N, D, K):
     g = gen(D + K + 1)
     X, C = (torch.randint(-1, 2, (n, D), generator=g, device=DEV).float() for n in (N, K))
